@@ -10,6 +10,16 @@ importing this package fails if the library cannot be loaded.
     conv2d_nhwc_fwd_f32(X, F)    the same with float32 tensors
     conv2d_nhwc_fwd_ex(X, F, b)  bf16 with stride, zero padding, dilation and a float32 bias
     depthwise_fwd(x, w, bias)    depthwise conv, float32 NCHW, exact or fast mode
+
+In 8-bit integers (signed bytes with a float32 scale per row), the K = 1 convolution and what
+feeds it:
+
+    conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias, norm)   dense 1 x 1 conv of bf16 X, quantised per pixel
+    rmsnorm_i8_fwd(x, weight, residual)              norm (and residual addition) -> 8-bit rows
+    quant_rows_i8_fwd(x, glu)                        rows, or silu(gate) * up, -> 8-bit rows
+    quant_filter_i8_fwd(F)                           filter [Cin,Cout] -> 8-bit rows [Cout,Cin]
+    pointwise_i8_fwd(q, q_scale, Wq, w_scale, bias)  their product
+    dequant_rows_i8_fwd(q, scale)                    8-bit rows back to bf16 or float32
 """
 from __future__ import annotations
 
@@ -27,6 +37,8 @@ CONV_ERR_DEVICE_TIMEOUT = -5
 CONV_ERR_DEVICE_BOUNDS = -6
 DW_EXACT = 0
 DW_FAST = 1
+CONV_BF16 = 0
+CONV_F32 = 1
 
 # CONV_B200_DEBUG_BOUNDS=1 at import loads the bounds-checked build of the same library (every
 # computed global access checked; a failure sets CONV_ERR_DEVICE_BOUNDS and skips the access)
@@ -56,6 +68,23 @@ lib.dwpw_fwd.argtypes = [_P] * 6 + [_I] * 10 + [_P]
 lib.dwpw_fwd.restype = _I
 lib.depthwise_fwd.argtypes = [_P, _P, _P, _P] + [_I] * 11 + [_P]
 lib.depthwise_fwd.restype = _I
+_F = ctypes.c_float
+lib.conv_i8_row_pitch.argtypes = [_I]
+lib.conv_i8_row_pitch.restype = _I
+lib.rmsnorm_i8_fwd.argtypes = [_P] * 6 + [_I] * 3 + [_F, _I, _P]
+lib.rmsnorm_i8_fwd.restype = _I
+lib.quant_rows_i8_fwd.argtypes = [_P] * 3 + [_I] * 5 + [_P]
+lib.quant_rows_i8_fwd.restype = _I
+lib.quant_filter_i8_fwd.argtypes = [_P] * 3 + [_I] * 4 + [_P]
+lib.quant_filter_i8_fwd.restype = _I
+lib.dequant_rows_i8_fwd.argtypes = [_P] * 3 + [_I] * 4 + [_P]
+lib.dequant_rows_i8_fwd.restype = _I
+lib.pointwise_i8_fwd.argtypes = [_P] * 6 + [_I] * 6 + [_P]
+lib.pointwise_i8_fwd.restype = _I
+lib.conv2d_nhwc_i8_workspace.argtypes = [_I] * 4
+lib.conv2d_nhwc_i8_workspace.restype = ctypes.c_size_t
+lib.conv2d_nhwc_fwd_i8.argtypes = [_P, _P, _F] + [_P] * 5 + [ctypes.c_size_t] + [_I] * 6 + [_P]
+lib.conv2d_nhwc_fwd_i8.restype = _I
 lib.conv_status_string.argtypes = [_I]
 lib.conv_status_string.restype = ctypes.c_char_p
 lib.conv_device_status.argtypes = [_P, _I]
@@ -76,7 +105,8 @@ EXPORTS = ("conv2d_nhwc_fwd", "conv2d_nhwc_fwd_f32", "conv2d_nhwc_fwd_ex", "conv
            "conv2d_nhwc_im2col_workspace", "conv2d_nhwc_fwd_im2col", "conv2d_nhwc_fwd_im2col_noalloc", "dwpw_fwd",
            "depthwise_fwd", "conv_status_string", "conv_device_status", "conv_last_kernel",
            "conv_selftest_wait_timeout", "conv_debug_bounds_build", "conv_debug_bounds_info",
-           "conv_selftest_bounds")
+           "conv_selftest_bounds", "conv_i8_row_pitch", "rmsnorm_i8_fwd", "quant_rows_i8_fwd", "quant_filter_i8_fwd",
+           "dequant_rows_i8_fwd", "pointwise_i8_fwd", "conv2d_nhwc_i8_workspace", "conv2d_nhwc_fwd_i8")
 CONV_IM2COL_STATIC_BYTES = 32 * 1024 * 1024   # the scratch of conv2d_nhwc_fwd_im2col_noalloc
 
 
@@ -374,6 +404,205 @@ def dwpw_fwd(x, w_dw, b_dw, F, b_pw=None, y=None, stride=1, pad=0, dil=1, mode=D
     _call(lib.dwpw_fwd, "dwpw_fwd", (x, w_dw, b_dw, F, b_pw, y), stream,
           px, pw, pbd, pf, pbp, py, N, C, H, W, K, stride, pad, dil, Cout, int(mode))
     return y
+
+
+def _i8_dtype(t, name):
+    """The conv_dtype of a bfloat16 or float32 tensor."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype == torch.bfloat16:
+        return CONV_BF16
+    if t.dtype == torch.float32:
+        return CONV_F32
+    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+
+
+def empty_rows_i8(rows, C, device="cuda"):
+    """An uninitialised int8 matrix [rows, C] in the layout the 8-bit operators take: rows start
+    on 16-byte boundaries, so the tensor is a view of [rows, pitch] where C is not a multiple of
+    16. Copy 8-bit rows from elsewhere (a checkpoint's filter) into one with copy_()."""
+    import torch
+    pitch = lib.conv_i8_row_pitch(int(C))
+    if pitch == 0 or rows < 1:
+        raise ValueError("rows and C must be positive")
+    return torch.empty((rows, pitch), dtype=torch.int8, device=device)[:, :C]
+
+
+def _rows_i8(t, name, rows=None, C=None):
+    """(pointer, row pitch) of an int8 matrix whose rows start on 16-byte boundaries."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int8:
+        raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    n, c = t.shape
+    if (rows is not None and n != rows) or (C is not None and c != C):
+        raise ValueError(f"{name} has the wrong shape")
+    # the stride of a dimension with one element means nothing
+    pitch = t.stride(0) if n > 1 else (c + 15) // 16 * 16
+    if (c > 1 and t.stride(1) != 1) or pitch < c or pitch % 16:
+        raise ValueError(f"{name} must be an int8 matrix whose rows are contiguous and start on 16-byte boundaries "
+                         "(empty_rows_i8 makes one)")
+    return t.data_ptr(), pitch
+
+
+def _scales(t, n, name):
+    p = _tensor(t, _f32(), 1, name)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries")
+    return p
+
+
+def _f32():
+    import torch
+    return torch.float32
+
+
+def _new_rows_i8(q, scale, rows, C, device):
+    """q and scale, allocated where None."""
+    import torch
+    if q is None:
+        q = empty_rows_i8(rows, C, device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=device)
+    return q, scale
+
+
+def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-6, stream=None):
+    """Root-mean-square norm of the rows of x [M, C] (bfloat16 or float32), with a residual's
+    addition before it, and 8-bit rows out: h = x + residual (rounded to x's type; x itself without
+    a residual), then h * weight / sqrt(mean(h^2) + eps) as int8 q [M, C] and float32 scale [M].
+    weight is float32 [C]. h may be x or residual (updated in place). Returns (q, scale, h); h is
+    None without a residual."""
+    import torch
+    dt = _i8_dtype(x, "x")
+    px = _tensor(x, x.dtype, 2, "x")
+    M, C = x.shape
+    pw = _scales(weight, C, "weight")
+    pr = ph = None
+    if residual is not None:
+        pr = _tensor(residual, x.dtype, 2, "residual")
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+        if h is None:
+            h = torch.empty_like(x)
+        elif h.shape != x.shape:
+            raise ValueError("h has the wrong shape")
+        ph = _tensor(h, x.dtype, 2, "h")
+    elif h is not None:
+        raise ValueError("h is x + residual: give the residual too")
+    q, scale = _new_rows_i8(q, scale, M, C, x.device)
+    pq, ldq = _rows_i8(q, "q", M, C)
+    ps = _scales(scale, M, "scale")
+    _call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", (x, residual, weight, h, q, scale), stream,
+          px, pr, pw, ph, pq, ps, M, C, ldq, float(eps), dt)
+    return q, scale, h
+
+
+def quant_rows_i8_fwd(x, glu=False, q=None, scale=None, stream=None):
+    """8-bit rows of x [M, C] (bfloat16 or float32): int8 q [M, C] and float32 scale [M], one per row.
+    With glu, x is [M, 2C] and the rows are silu(x[:, :C]) * x[:, C:]. Returns (q, scale)."""
+    dt = _i8_dtype(x, "x")
+    px = _tensor(x, x.dtype, 2, "x")
+    M, C = x.shape
+    if glu:
+        if C % 2:
+            raise ValueError("glu needs x [M, 2C]")
+        C //= 2
+    q, scale = _new_rows_i8(q, scale, M, C, x.device)
+    pq, ldq = _rows_i8(q, "q", M, C)
+    ps = _scales(scale, M, "scale")
+    _call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", (x, q, scale), stream, px, pq, ps, M, C, ldq, 1 if glu else 0, dt)
+    return q, scale
+
+
+def quant_filter_i8_fwd(F, q=None, scale=None, stream=None):
+    """8-bit rows of a 1 x 1 filter F [Cin, Cout] or [1, 1, Cin, Cout] (bfloat16 or float32): int8
+    q [Cout, Cin], transposed, and float32 scale [Cout], one per output channel. Returns (q, scale)."""
+    dt = _i8_dtype(F, "F")
+    if F.dim() == 4 and tuple(F.shape[:2]) != (1, 1):
+        raise ValueError("F must be a 1 x 1 filter")
+    pf = _tensor(F, F.dtype, 4 if F.dim() == 4 else 2, "F")
+    Cin, Cout = F.shape[-2:]
+    q, scale = _new_rows_i8(q, scale, Cout, Cin, F.device)
+    pq, ldw = _rows_i8(q, "q", Cout, Cin)
+    ps = _scales(scale, Cout, "scale")
+    _call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", (F, q, scale), stream, pf, pq, ps, Cin, Cout, ldw, dt)
+    return q, scale
+
+
+def dequant_rows_i8_fwd(q, scale, y=None, dtype=None, stream=None):
+    """Reads 8-bit rows back: y [M, C] = q * scale, in y's type (dtype, bfloat16 by default)."""
+    pq, ldq = _rows_i8(q, "q")
+    M, C = q.shape
+    ps = _scales(scale, M, "scale")
+    y = _output(y, dtype, (M, C), q.device)
+    dt = _i8_dtype(y, "y")
+    py = _tensor(y, y.dtype, 2, "y")
+    _call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", (q, scale, y), stream, pq, ps, py, M, C, ldq, dt)
+    return y
+
+
+def _output(y, dtype, shape, device):
+    import torch
+    if y is None:
+        return torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+    if tuple(y.shape) != shape or (dtype is not None and y.dtype != dtype):
+        raise ValueError("y has the wrong shape or type")
+    return y
+
+
+def pointwise_i8_fwd(q, q_scale, Wq, w_scale, bias=None, y=None, dtype=None, stream=None):
+    """The product of 8-bit rows: y [M, Cout] = (q [M, Cin] @ Wq [Cout, Cin]^T) * q_scale [M] * w_scale [Cout]
+    + bias [Cout], the sum exact in int32, in y's type (dtype, bfloat16 by default)."""
+    pq, ldq = _rows_i8(q, "q")
+    M, Cin = q.shape
+    pw, ldw = _rows_i8(Wq, "Wq", None, Cin)
+    Cout = Wq.shape[0]
+    ps, pws = _scales(q_scale, M, "q_scale"), _scales(w_scale, Cout, "w_scale")
+    pb = None if bias is None else _scales(bias, Cout, "bias")
+    y = _output(y, dtype, (M, Cout), q.device)
+    dt = _i8_dtype(y, "y")
+    py = _tensor(y, y.dtype, 2, "y")
+    _call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", (q, q_scale, Wq, w_scale, bias, y), stream,
+          pq, ps, pw, pws, pb, py, M, Cin, Cout, ldq, ldw, dt)
+    return y
+
+
+def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, workspace=None, stream=None):
+    """Dense NHWC 1 x 1 convolution in 8-bit integers: X bfloat16 [N,H,W,Cin], quantised per pixel
+    (with norm, float32 [Cin]: after a root-mean-square norm with that weight), times the filter Wq
+    int8 [Cout, Cin] with w_scale [Cout] (quant_filter_i8_fwd) -> Y bfloat16 [N,H,W,Cout].
+    workspace: a uint8 CUDA tensor of at least conv2d_nhwc_i8_workspace bytes, allocated here if None."""
+    import torch
+    px = _tensor(X, torch.bfloat16, 4, "X")
+    N, H, W, Cin = X.shape
+    pw, ldw = _rows_i8(Wq, "Wq", None, Cin)
+    Cout = Wq.shape[0]
+    pws = _scales(w_scale, Cout, "w_scale")
+    pb = None if bias is None else _scales(bias, Cout, "bias")
+    pn = None if norm is None else _scales(norm, Cin, "norm")
+    if workspace is None:
+        need = lib.conv2d_nhwc_i8_workspace(N, H, W, Cin)
+        if need == 0:
+            raise ValueError("invalid shape")
+        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if Y is None:
+        Y = torch.empty((N, H, W, Cout), dtype=torch.bfloat16, device=X.device)
+    elif tuple(Y.shape) != (N, H, W, Cout):
+        raise ValueError("Y has the wrong shape")
+    py = _tensor(Y, torch.bfloat16, 4, "Y")
+    _call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", (X, norm, Wq, w_scale, bias, Y, workspace), stream,
+          px, pn, float(eps), pw, pws, pb, py, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+          N, H, W, Cin, Cout, ldw)
+    return Y
 
 
 def conv_last_kernel() -> str:

@@ -31,6 +31,9 @@
 #include "depthwise_plane.cuh"
 #include "dwpw.cuh"
 #include "dwpw_gemm.cuh"
+#include "i8_rows.cuh"
+#include "i8_filter.cuh"
+#include "i8_gemm.cuh"
 #include "ptx.cuh"
 
 namespace convb200 {
@@ -2141,3 +2144,5 @@ int dwpw_fwd(const float *x, const float *w_dw, const float *b_dw, const void *F
 }
 
 }  // extern "C"
+
+#include "capi_i8.cuh"   // the 8-bit entry points

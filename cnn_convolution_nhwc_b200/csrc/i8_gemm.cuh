@@ -1,0 +1,474 @@
+// The 1 x 1 convolution (matrix product) in 8-bit integers:
+//     Y[m][n] = (sum_k q[m][k] * Wq[n][k]) * q_scale[m] * w_scale[n] + bias[n]
+// with the sum exact in int32 (|q|, |Wq| <= 128 and at most 131071 terms), the scales and the bias
+// applied in float32 and one rounding to the output type. Both operands run along k, so both are
+// staged by plain 2-D tensor copies of 128-byte rows (128 values, 128-byte swizzle) and multiplied
+// by tcgen05.mma kind::i8, K = 32 values a step; rows, columns and k past the matrices read as
+// zeros (the tensor maps' extents are exact), so no size has a special case in the main loop.
+//
+// Two kernels. With many tokens the tensor cores bound the product, and a CTA pair computes a
+// 256 x 256 tile. With few, the filter's bytes bound it: the filter's rows become the 128 rows of
+// the MMA, the tokens its 16 to 128 columns, and the reduction is split over a cluster until the
+// GPU is full.
+#pragma once
+#include <cuda_bf16.h>
+
+#include "dense_halo.cuh"
+#include "i8_rows.cuh"
+#include "ptx.cuh"
+
+namespace convb200 {
+
+struct I8GemmParams {
+    const float *q_scale;   // [M]
+    const float *w_scale;   // [N]
+    const float *bias;      // [N] or null
+    void *Y;                // [M][N]
+    int M, N;
+    int num_kblk;           // ceil(Cin / 128)
+    int n_tiles;            // tiles along N
+    int m_tiles;            // tiles along M
+    int split;              // CTAs per cluster, each with its share of the k blocks (split kernel)
+    int num_tiles;
+    int vec;                // 16-byte stores: rows of Y on 16-byte boundaries
+};
+
+__device__ __forceinline__ void i8_out(float *p, float v) { *p = v; }
+__device__ __forceinline__ void i8_out(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// ---------------------------------------------------------------------------------------
+// Few tokens: i8_split_kernel
+// ---------------------------------------------------------------------------------------
+// One CTA per (128 filter rows, BN tokens, share of the k blocks). Every CTA of a cluster
+// accumulates its share in TMEM, sends each token column to the CTA of the cluster that owns it
+// (distributed shared memory), and after one cluster barrier the owners add the shares, which are
+// integers: the result does not depend on the split.
+//   warp 0      TMA: one slot (128 filter rows and BN token rows of 128 bytes) per k block
+//   warp 1      TMEM allocation, MMA issue (M = 128, N = BN)
+//   warps 2..5  epilogue, one TMEM lane quarter each
+template <int BN_, int STAGES_>
+struct I8SplitCfg {
+    static constexpr int BN = BN_, STAGES = STAGES_;
+    static constexpr int W_BYTES = 128 * 128, Q_BYTES = BN * 128;
+    static constexpr int SLOT = W_BYTES + Q_BYTES;
+    static constexpr int RECV_BYTES = BN * 128 * 4;   // the owned columns' shares: split x (BN / split) x 128
+    static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
+    static constexpr int SMEM = 1024 + STAGES * SLOT + RECV_BYTES + BN * 4 + (2 * STAGES + 1) * 8 + 16;
+    static constexpr int THREADS = 192;
+    static constexpr uint32_t IDESC = idesc_i8_s32(128, BN);
+};
+
+template <class Cfg, typename OUT>
+__global__ void __launch_bounds__(Cfg::THREADS)
+i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmQ, const I8GemmParams p,
+                unsigned int *status) {
+    grid_dependents_launch();
+    constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw_base);
+    const uint32_t recv = base + STAGES * Cfg::SLOT;
+    float *s_scale = reinterpret_cast<float *>(smem + STAGES * Cfg::SLOT + Cfg::RECV_BYTES);
+    const uint32_t bars = recv + Cfg::RECV_BYTES + BN * 4;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (STAGES + s); };
+    const uint32_t accf = bars + 8u * (2 * STAGES);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + (accf + 8u - base));
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t S = static_cast<uint32_t>(p.split);
+    const uint32_t rank = S > 1 ? cluster_rank() : 0u;
+    const int tile = static_cast<int>(blockIdx.x / S);
+    const int mt = tile / p.n_tiles;
+    const int n0 = (tile - mt * p.n_tiles) * 128, m0 = mt * BN;
+    const int kb0 = static_cast<int>(1LL * p.num_kblk * rank / S), kb1 = static_cast<int>(1LL * p.num_kblk * (rank + 1) / S);
+    const int cols = p.M - m0 < BN ? p.M - m0 : BN;   // tokens of this tile
+    const int own = BN / static_cast<int>(S);         // columns a CTA of the cluster owns
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(accf, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmQ);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_holder), Cfg::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    // the peers' shared memory may be written once they have arrived here
+    if (S > 1) cluster_arrive();
+    grid_dependency_wait();
+
+    if (warp == 0) {
+        bool ok = true;
+        uint32_t s = 0, ph = 0;
+        int issued = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(empty(s), ph ^ 1u)) { ok = false; break; }
+            if (lane == 0) {
+                const uint32_t slot = base + s * Cfg::SLOT;
+                mbar_arrive_expect_tx(full(s), Cfg::SLOT);
+                tma_load_2d(slot, &tmW, full(s), kb * 128, n0);
+                tma_load_2d(slot + Cfg::W_BYTES, &tmQ, full(s), kb * 128, m0);
+            }
+            __syncwarp();
+            ++issued;
+            if (++s == STAGES) { s = 0; ph ^= 1u; }
+        }
+        if (!ok && lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
+        // every copy has landed before the CTA may exit
+        for (int j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
+            if (!mbar_wait_warp(full(j % STAGES), (j / STAGES) & 1)) {
+                if (lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
+                break;
+            }
+    } else if (warp == 1) {
+        const uint32_t leader = elect_one_sync();
+        bool ok = true;
+        uint32_t s = 0, ph = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!mbar_wait_warp(full(s), ph)) { ok = false; break; }
+            tc_fence_after();
+            const uint64_t a = smem_desc_sw128(base + s * Cfg::SLOT, 16, 1024);
+            const uint64_t b = smem_desc_sw128(base + s * Cfg::SLOT + Cfg::W_BYTES, 16, 1024);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)   // 32 bytes of k a step: +2 in the descriptors' 16-byte units
+                umma_i8_ss_if(tmem_base, a + 2 * j, b + 2 * j, Cfg::IDESC, (kb > kb0 || j > 0) ? 1u : 0u, leader);
+            umma_commit_if(empty(s), leader);
+            if (++s == STAGES) { s = 0; ph ^= 1u; }
+        }
+        if (!ok && lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
+        umma_commit_if(accf, leader);
+        // all MMAs are complete before TMEM is freed
+        if (!mbar_wait_warp(accf, 0) && lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
+    } else {
+        const int t = threadIdx.x - 64;
+        for (int j = t; j < cols; j += 128)
+            s_scale[j] = in_bounds(m0 + j, 1, p.M, kSiteI8GemmScale, status) ? p.q_scale[m0 + j] : 0.0f;
+        if (!mbar_wait_warp(accf, 0) && lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
+    }
+    tc_fence_before();
+    __syncthreads();   // also publishes s_scale
+    tc_fence_after();
+
+    const int quarter = warp & 3;            // TMEM lanes of this warp (warps 2..5)
+    const int n_lane = quarter * 32 + lane;  // filter row inside the tile
+    const int n = n0 + n_lane;
+    const bool live = warp >= 2 && !*abort_flag;
+    float ws = 0.0f, bias = 0.0f;
+    OUT *Y = static_cast<OUT *>(p.Y);
+    const long long y_elems = 1LL * p.M * p.N;
+    if (live && n < p.N && in_bounds(n, 1, p.N, kSiteI8GemmScale, status)) {
+        ws = p.w_scale[n];
+        if (p.bias) bias = p.bias[n];
+    }
+    auto put = [&](int j, int acc) {   // column j of the tile
+        const long long at = 1LL * (m0 + j) * p.N + n;
+        const float v = static_cast<float>(acc) * s_scale[j] * ws;
+        if (n < p.N && in_bounds(at, 1, y_elems, kSiteI8GemmY, status)) i8_out(Y + at, p.bias ? v + bias : v);
+    };
+    const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    if (S > 1) cluster_wait();
+    if (live) {
+#pragma unroll 1
+        for (int j0 = 0; j0 < cols; j0 += 16) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_row + j0, r);
+            tmem_wait_ld();
+            if (S == 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (j0 + j < cols) put(j0 + j, static_cast<int>(r[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int col = j0 + j;
+                    if (col >= cols) break;
+                    const uint32_t to = static_cast<uint32_t>(col / own);
+                    const uint32_t at = recv + ((rank * own + (col - to * own)) * 128 + n_lane) * 4;
+                    st_cluster_u32(map_rank(at, to), r[j]);
+                }
+            }
+        }
+    }
+    if (S > 1) {
+        cluster_sync_all();
+        const int c0 = static_cast<int>(rank) * own;
+        if (live) {
+            for (int j = 0; j < own && c0 + j < cols; ++j) {
+                int acc = 0;
+                for (uint32_t r = 0; r < S; ++r) {
+                    int v;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(recv + ((r * own + j) * 128 + n_lane) * 4));
+                    acc += v;
+                }
+                put(c0 + j, acc);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem_base, Cfg::TMEM_COLS);
+}
+
+// ---------------------------------------------------------------------------------------
+// Many tokens: i8_pair_kernel
+// ---------------------------------------------------------------------------------------
+// A persistent CTA pair per 256 x 256 tile of Y (M = 256, N = 256 MMAs, cta_group::2): each CTA
+// stages 128 token rows and 128 filter rows per k block and receives its 128 tokens x 256 columns
+// of the accumulator. Two accumulators of 256 columns fill TMEM, so tile t + 1 multiplies while
+// tile t is scaled and stored.
+//   warp 0      TMA ring of STAGES slots (16 KB of tokens + 16 KB of filter per CTA)
+//   warp 1      TMEM allocation; the even CTA's issues the MMAs for both
+//   warps 2..9  epilogue, two warps per TMEM lane quarter taking alternate chunks of 128 bytes of
+//               output: tcgen05.ld, scale, round, swizzled staging, 16-byte stores
+struct I8PairCfg {
+    static constexpr int BM = 128, BN = 256, STAGES = 6;   // per CTA: 128 rows; the pair: 256
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, SLOT = A_BYTES + B_BYTES;
+    static constexpr int NUM_EPI = 8;
+    static constexpr int EPI_BYTES = NUM_EPI * 32 * 128;
+    static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
+    static constexpr int SMEM = 1024 + STAGES * SLOT + EPI_BYTES + NUM_BARS * 8 + 16;
+    static constexpr int THREADS = 32 * (2 + NUM_EPI);
+    static constexpr uint32_t IDESC = idesc_i8_s32(256, BN);
+    static constexpr int GROUP = 8;   // row tiles walked together
+};
+static_assert(I8PairCfg::SMEM <= 232448, "shared memory of one CTA");
+
+// Tile t of the walk: GROUP row tiles together, so that the CTAs in flight share their operands
+// in L2 (74 pairs in flight hold about 8 x 9 tiles).
+__device__ __forceinline__ void i8_tile(int t, int m_tiles, int n_tiles, int &mt, int &nt) {
+    const int per = I8PairCfg::GROUP * n_tiles;
+    const int g = t / per, r = t - g * per;
+    const int m_first = g * I8PairCfg::GROUP;
+    const int h = m_tiles - m_first < I8PairCfg::GROUP ? m_tiles - m_first : I8PairCfg::GROUP;
+    nt = r / h;
+    mt = m_first + (r - nt * h);
+}
+
+template <typename OUT>
+__global__ void __launch_bounds__(I8PairCfg::THREADS, 1)
+i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmW, const I8GemmParams p,
+               unsigned int *status) {
+    using Cfg = I8PairCfg;
+    grid_dependents_launch();
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw_base);
+    constexpr uint32_t epi_off = Cfg::STAGES * Cfg::SLOT;
+    const uint32_t bars = base + epi_off + Cfg::EPI_BYTES;
+    auto full = [&](int s) { return bars + 8u * s; };
+    auto empty = [&](int s) { return bars + 8u * (Cfg::STAGES + s); };
+    auto accf = [&](int b) { return bars + 8u * (2 * Cfg::STAGES + b); };
+    auto acce = [&](int b) { return bars + 8u * (2 * Cfg::STAGES + 2 + b); };
+    const uint32_t done_bar = bars + 8u * (2 * Cfg::STAGES + 4);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + epi_off + Cfg::EPI_BYTES + Cfg::NUM_BARS * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    auto lead = [&](uint32_t a) { return map_rank(a, 0u); };
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(accf(b), 1);
+            mbar_init(acce(b), 2 * Cfg::NUM_EPI);   // one arrival per epilogue warp of both CTAs
+        }
+        mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmW);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // both CTAs' barriers and TMEM exist before either is used
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    grid_dependency_wait();
+
+    auto fail = [&]() {
+        atomicOr(status, kStatusTimeout);
+        *abort_flag = 1;
+        st_cluster_u32(map_rank(smem_u32(const_cast<int *>(abort_flag)), rank ^ 1u), 1u);
+    };
+    const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
+
+    if (warp == 0) {
+        uint32_t it = 0, s = 0, ph = 0;
+        bool ok = true;
+        for (int t = first; t < p.num_tiles && ok && !*abort_flag; t += step) {
+            int mt, nt;
+            i8_tile(t, p.m_tiles, p.n_tiles, mt, nt);
+            const int row_q = mt * 256 + static_cast<int>(rank) * 128, row_w = nt * 256 + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < p.num_kblk; ++kb, ++it) {
+                if (!mbar_wait_warp(empty(s), ph ^ 1u)) { ok = false; break; }
+                if (lane == 0) {
+                    const uint32_t slot = base + s * Cfg::SLOT;
+                    if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * Cfg::SLOT);   // both CTAs' copies
+                    tma_load_2d_pair(slot, &tmQ, lead(full(s)), kb * 128, row_q);
+                    tma_load_2d_pair(slot + Cfg::A_BYTES, &tmW, lead(full(s)), kb * 128, row_w);
+                }
+                __syncwarp();
+                if (++s == Cfg::STAGES) { s = 0; ph ^= 1u; }
+            }
+        }
+        if (!ok && lane == 0) fail();
+        // drain: every copy issued has been consumed (the even CTA's commits report to both)
+        for (uint32_t j = it > (uint32_t)Cfg::STAGES ? it - Cfg::STAGES : 0u; j < it; ++j)
+            if (!mbar_wait_warp(empty(j % Cfg::STAGES), (j / Cfg::STAGES) & 1u)) { if (lane == 0) fail(); break; }
+    } else if (warp == 1) {
+        const uint32_t leader = elect_one_sync();
+        constexpr uint16_t kBoth = 0x3;
+        if (rank == 0) {
+            uint32_t local = 0, s = 0, ph = 0;
+            bool ok = true;
+            const uint64_t a0 = smem_desc_sw128(base, 16, 1024);
+            const uint64_t b0 = smem_desc_sw128(base + Cfg::A_BYTES, 16, 1024);
+            for (int t = first; t < p.num_tiles && ok && !__any_sync(0xffffffffu, *abort_flag != 0); t += step, ++local) {
+                const uint32_t b = local & 1u;
+                if (!mbar_wait_warp(acce(b), ((local >> 1) & 1u) ^ 1u)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d = tmem_base + b * Cfg::BN;
+                for (int kb = 0; kb < p.num_kblk; ++kb) {
+                    if (!mbar_wait_warp(full(s), ph)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t ad = a0 + s * (Cfg::SLOT >> 4), bd = b0 + s * (Cfg::SLOT >> 4);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        umma_i8_ss_pair_if(d, ad + 2 * j, bd + 2 * j, Cfg::IDESC, (kb > 0 || j > 0) ? 1u : 0u, leader);
+                    umma_commit_pair_if(empty(s), kBoth, leader);
+                    if (++s == Cfg::STAGES) { s = 0; ph ^= 1u; }
+                }
+                if (!ok) break;
+                umma_commit_pair_if(accf(b), kBoth, leader);
+            }
+            __syncwarp();
+            if (!ok && lane == 0) fail();
+            // all MMAs complete before TMEM is released
+            umma_commit_pair_if(done_bar, kBoth, leader);
+            if (!mbar_wait_warp(done_bar, 0) && lane == 0) fail();
+        }
+    } else {
+        constexpr int CW = 128 / static_cast<int>(sizeof(OUT));   // columns of a 128-byte chunk
+        constexpr int V = 16 / static_cast<int>(sizeof(OUT));     // values of a 16-byte store
+        const int quarter = warp & 3, eg = (warp - 2) >> 2;
+        const uint32_t stage = base + epi_off + (warp - 2) * 4096;
+        OUT *Y = static_cast<OUT *>(p.Y);
+        const long long y_elems = 1LL * p.M * p.N;
+        uint32_t local = 0;
+        for (int t = first; t < p.num_tiles; t += step, ++local) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const uint32_t b = local & 1u;
+            int mt, nt;
+            i8_tile(t, p.m_tiles, p.n_tiles, mt, nt);
+            const int row0 = mt * 256 + static_cast<int>(rank) * 128 + quarter * 32;   // this warp's 32 rows
+            const int n0 = nt * 256;
+            const float qs = row0 + lane < p.M ? p.q_scale[row0 + lane] : 0.0f;
+            if (!mbar_wait_warp_backoff(accf(b), (local >> 1) & 1u, 64)) { if (lane == 0) fail(); break; }
+            tc_fence_after();
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * Cfg::BN;
+#pragma unroll 1
+            for (int h = eg; h < Cfg::BN / CW; h += 2) {
+                const int c0 = n0 + h * CW;
+                if (c0 >= p.N) break;
+                // the scales and biases of the chunk's columns, CW / 32 a lane
+                float wsv[CW / 32], bv[CW / 32];
+#pragma unroll
+                for (int i = 0; i < CW / 32; ++i) {
+                    const int c = c0 + i * 32 + lane;
+                    wsv[i] = c < p.N ? p.w_scale[c] : 0.0f;
+                    bv[i] = c < p.N && p.bias ? p.bias[c] : 0.0f;
+                }
+#pragma unroll
+                for (int g = 0; g < CW / 16; ++g) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(t_row + h * CW + g * 16, r);
+                    tmem_wait_ld();
+                    float v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int from = (g * 16 + j) & 31;
+                        const float w = __shfl_sync(0xffffffffu, wsv[g / 2], from);
+                        v[j] = static_cast<float>(static_cast<int>(r[j])) * qs * w;
+                        if (p.bias) v[j] += __shfl_sync(0xffffffffu, bv[g / 2], from);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16 / V; ++i) {
+                        const uint32_t c = g * (16 / V) + i;   // 16-byte piece of the lane's 128-byte row
+                        const float *u = v + i * V;
+                        const uint32_t at = stage + lane * 128 + ((c ^ (lane & 7)) << 4);
+                        if constexpr (sizeof(OUT) == 2)
+                            st_shared_v4(at, halo_pack_bf16x2(u[0], u[1]), halo_pack_bf16x2(u[2], u[3]),
+                                         halo_pack_bf16x2(u[4], u[5]), halo_pack_bf16x2(u[6], u[7]));
+                        else
+                            st_shared_v4(at, __float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]),
+                                         __float_as_uint(u[3]));
+                    }
+                }
+                __syncwarp();
+                if (p.vec) {   // 8 lanes a row, 4 rows an instruction
+                    const int col = c0 + (lane & 7) * V;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int rr = i * 4 + (lane >> 3), row = row0 + rr;
+                        const long long at = 1LL * row * p.N + col;
+                        if (row < p.M && col < p.N && in_bounds(at, V, y_elems, kSiteI8GemmY, status)) {
+                            uint32_t a, bb, c, d;
+                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(a), "=r"(bb), "=r"(c), "=r"(d)
+                                         : "r"(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)));
+                            *reinterpret_cast<uint4 *>(Y + at) = make_uint4(a, bb, c, d);
+                        }
+                    }
+                } else {       // an element a lane, a row at a time
+                    for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr) {
+#pragma unroll
+                        for (int i = 0; i < CW / 32; ++i) {
+                            const int e = i * 32 + lane, col = c0 + e;
+                            const long long at = 1LL * (row0 + rr) * p.N + col;
+                            if (col < p.N && in_bounds(at, 1, y_elems, kSiteI8GemmY, status))
+                                Y[at] = *reinterpret_cast<const OUT *>(
+                                    smem + epi_off + (warp - 2) * 4096 + rr * 128 + (((e / V) ^ (rr & 7)) << 4) +
+                                    (e % V) * sizeof(OUT));
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            // the accumulator may be overwritten by the next tile but one
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(lead(acce(b)));
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // neither CTA leaves while the other may still signal its barriers
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+}
+
+}  // namespace convb200

@@ -22,6 +22,8 @@ enum BoundsSite : unsigned {
     kSiteDirectX = 1, kSiteDirectY, kSiteFoldY, kSiteHaloY, kSiteStreamY, kSiteTcBias, kSiteDwY, kSiteDwRegX,
     kSiteDwRegY, kSiteDwTmaY, kSiteDwPlaneX, kSiteDwPlaneY, kSiteDwPwX, kSiteDwPwY, kSiteDwPwGemmX,
     kSiteDwPwGemmW, kSiteDwPwGemmY, kSiteIm2colX, kSiteIm2colA, kSiteDwTmaX, kSiteDwX, kSiteHaloPadBias, kSiteHaloPadY,
+    kSiteI8RowsX, kSiteI8RowsQ, kSiteI8RowsScale, kSiteI8FilterF, kSiteI8FilterQ, kSiteI8FilterScale, kSiteI8Dequant,
+    kSiteI8GemmScale, kSiteI8GemmY,
     kSiteSelftest = 255
 };
 #ifdef CONV_DEBUG_BOUNDS
@@ -169,6 +171,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The two halves of cluster_sync_all, for work between them.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // shared::cta address -> the same offset in cluster rank `rank`'s shared memory
@@ -347,6 +358,20 @@ __device__ __forceinline__ void umma_f16_ss_if(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
+// D[tmem] (+)= A[smem] * B[smem], kind::i8 (8-bit integers, 32-bit integer accumulator), in a
+// converged warp as above.
+__device__ __forceinline__ void umma_i8_ss_if(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        :
+        : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
 // umma_commit by the lane whose `leader` is non-zero, in a converged warp.
 __device__ __forceinline__ void umma_commit_if(uint32_t bar, uint32_t leader) {
     asm volatile(
@@ -380,6 +405,18 @@ __device__ __forceinline__ void umma_f16_ss_pair_if(uint32_t d_tmem, uint64_t a_
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 q, %5, 0;\n\t"
         "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :
+        : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_i8_ss_pair_if(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                   uint32_t accumulate, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
         :
         : "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
@@ -448,6 +485,13 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_major) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Instruction descriptor for kind::i8 with signed 8-bit A and B, both K-major, and 32-bit integer D
+// (2 in the D format field, no saturation).
+__host__ __device__ constexpr uint32_t idesc_i8_s32(int M, int N) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // The same with an MN-major A operand as well (bit 15).

@@ -23,6 +23,10 @@
  *     Moving Across a Signal", section "Build an image-gradient map, one number at a time":
  *         out = floor((in + 2*pad - (dil*(k-1) + 1)) / stride) + 1.
  *
+ * The K = 1 case of the first in 8-bit integers -- quantisation of rows (with a root-mean-square
+ * norm or a gate before it) and of filters, the product, and both as one call
+ * (conv2d_nhwc_fwd_i8) -- is declared together further down.
+ *
  * Around them: the dense operation with stride, padding, dilation and bias (conv2d_nhwc_fwd_ex),
  * with channel groups, KH x KW filters and per-axis geometry, Conv1D included
  * (conv2d_nhwc_fwd_grouped), a depthwise pass fused with the pointwise pass after it (dwpw_fwd),
@@ -51,6 +55,7 @@
 #define CONV_B200_H
 
 #include <cuda_runtime_api.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -245,6 +250,105 @@ int depthwise_fwd(const float *x, const float *w, const float *bias, float *y,
 int dwpw_fwd(const float *x, const float *w_dw, const float *b_dw, const void *F, const float *b_pw, float *y,
              int N, int C, int H, int W, int K, int stride, int pad, int dil, int Cout, int mode,
              cudaStream_t stream);
+
+/*
+ * ---- 8-bit integers --------------------------------------------------------------------------
+ * The 1 x 1 convolution -- the product over the channels of every pixel, frame or token -- with
+ * both operands held as signed bytes: a scale per row (token) of the activations and per output
+ * channel of the filter. These have no counterpart on the pages; they extend conv2d_nhwc_fwd at
+ * K = 1, where a byte instead of a bf16 value halves the filter's traffic and doubles the tensor
+ * cores' rate.
+ *
+ * 8-bit rows: a matrix of M rows of C bytes is int8_t q[M][ld] with ld >= C bytes from row to
+ * row, ld a multiple of 16 and q 16-byte aligned (conv_i8_row_pitch(C) is the smallest such ld; 0
+ * for a C out of range). The bytes between C and ld are neither read nor written. A row's values
+ * are q[c] * scale.
+ *
+ * Rounding of a row v with A = max |v[c]| > 0: q[c] is 127 v[c] / A rounded to the nearest integer,
+ * ties to even (the real quotient of the float32 values, whatever the shape), scale = A / 127. A row
+ * of zeros has q = 0 and scale = 0. A row with a NaN or an infinity in v has q = 0 and scale = NaN,
+ * and so everything computed from it is NaN.
+ *
+ * Rules for all of them, besides the common ones: M (rows) and C may be of any size whose rows fit
+ * (offsets are 64-bit); dtype is a conv_dtype (other values: CONV_ERR_INVALID_ARG); a pitch below
+ * the row's length is CONV_ERR_INVALID_ARG, a pitch or a row pointer off the 16-byte rule
+ * CONV_ERR_MISALIGNED; other pointers are aligned to their element. Results do not depend on the
+ * shape of the launch: no atomics, one order per sum (integers in the product).
+ */
+typedef enum {
+    CONV_BF16 = 0,
+    CONV_F32 = 1
+} conv_dtype;
+
+int conv_i8_row_pitch(int C);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it and 8-bit rows out:
+ *     h = x + residual rounded to dtype (x without a residual),
+ *     v[c] = h[c] * weight[c],  rstd = 1 / sqrt(sum_c h[c]^2 / C + eps),
+ *     q, A from v as above,  scale = A * rstd / 127   (the norm's factor is in the scale only).
+ *   x, residual, h : dtype [M][C]; residual and h both NULL (no residual), or both given. h may be
+ *                    x or residual itself (updated in place); other overlaps are rejected
+ *   weight         : float32 [C]
+ *   q, scale       : 8-bit rows [M][ldq], float32 [M]
+ * The sum of squares is float32; a row where it passes the float32 range has q = 0 and scale = NaN.
+ * Requirements: M, C >= 1; eps a normal positive float.
+ */
+int rmsnorm_i8_fwd(const void *x, const void *residual, const float *weight, void *h, int8_t *q, float *scale,
+                   int M, int C, int ldq, float eps, int dtype, cudaStream_t stream);
+
+/*
+ * 8-bit rows of activations: v = x (glu = 0, x is dtype [M][C]), or the gated product of a
+ * feed-forward pair (glu = 1, x is dtype [M][2C], its halves gate and up):
+ *     v[c] = silu(x[c]) * x[C + c],  silu(a) = a / (1 + exp(-a)), in float32.
+ * Also quantises a filter stored [Cout][Cin] (a row per output channel).
+ */
+int quant_rows_i8_fwd(const void *x, int8_t *q, float *scale, int M, int C, int ldq, int glu, int dtype,
+                      cudaStream_t stream);
+
+/*
+ * A 1 x 1 filter of this library's layout, F dtype [Cin][Cout], to 8-bit rows per output channel:
+ * Wq [Cout][ldw] (transposed), scale [Cout]. Done once when a network is loaded.
+ * Requirements: Cin, Cout >= 1; Cin <= 131071 (else CONV_ERR_UNSUPPORTED).
+ */
+int quant_filter_i8_fwd(const void *F, int8_t *Wq, float *scale, int Cin, int Cout, int ldw, int dtype,
+                        cudaStream_t stream);
+
+/* Reads 8-bit rows back: y[m][c] = q[m][c] * scale[m] rounded to dtype; y is [M][C], contiguous. */
+int dequant_rows_i8_fwd(const int8_t *q, const float *scale, void *y, int M, int C, int ldq, int dtype,
+                        cudaStream_t stream);
+
+/*
+ * The product: Y[m][n] = (sum_c q[m][c] * Wq[n][c]) * q_scale[m] * w_scale[n] + bias[n].
+ *   q, q_scale  : 8-bit rows [M][ldq] of the activations, float32 [M]
+ *   Wq, w_scale : 8-bit rows [Cout][ldw] of the filter, float32 [Cout]
+ *   bias        : float32 [Cout] or NULL
+ *   Y           : dtype [M][Cout], contiguous
+ * The sum is exact (int32); scales and bias are applied in float32 in the order written, and the
+ * result is rounded once. Bytes of -128 are allowed.
+ * Requirements: M, Cin, Cout >= 1; Cin <= 131071 (else CONV_ERR_UNSUPPORTED).
+ */
+int pointwise_i8_fwd(const int8_t *q, const float *q_scale, const int8_t *Wq, const float *w_scale,
+                     const float *bias, void *Y, int M, int Cin, int Cout, int ldq, int ldw, int dtype,
+                     cudaStream_t stream);
+
+/*
+ * conv2d_nhwc_fwd at K = 1 in 8-bit integers: quantises every pixel's channels (norm NULL), or
+ * applies the root-mean-square norm over them first (norm: its weight, float32 [Cin]; eps), and
+ * multiplies by the quantised filter. Two launches on `stream`: quant_rows_i8_fwd or rmsnorm_i8_fwd
+ * into the workspace, then pointwise_i8_fwd, with exactly their results.
+ *   X : bfloat16 [N][H][W][Cin];  Y : bfloat16 [N][H][W][Cout]
+ *   Wq [Cout][ldw], w_scale, bias : as pointwise_i8_fwd
+ *   workspace : DEVICE memory, at least conv2d_nhwc_i8_workspace() bytes, 16-byte aligned, not
+ *               overlapping the tensors; overwritten. Calls that may run at the same time
+ *               (different streams) need one each.
+ * eps is ignored without norm. Requirements: N, H, W, Cin, Cout >= 1; N*H*W below 2^31 and
+ * Cin <= 131071 (else CONV_ERR_UNSUPPORTED).
+ */
+size_t conv2d_nhwc_i8_workspace(int N, int H, int W, int Cin);   /* 0 if invalid or unsupported */
+int conv2d_nhwc_fwd_i8(const void *X, const float *norm, float eps, const int8_t *Wq, const float *w_scale,
+                       const float *bias, void *Y, void *workspace, size_t workspace_bytes,
+                       int N, int H, int W, int Cin, int Cout, int ldw, cudaStream_t stream);
 
 /* Static English text for a conv_status value (never NULL). */
 const char *conv_status_string(int status);
