@@ -406,35 +406,38 @@ def dwpw_fwd(x, w_dw, b_dw, F, b_pw=None, y=None, stride=1, pad=0, dil=1, mode=D
     return y
 
 
-def _i8_dtype(t, name):
+# ---- 8-bit operators ---------------------------------------------------------------------
+# Their single-token calls take a few microseconds on the GPU, so these wrappers keep to a few on
+# the host: one test per tensor on the good path (the messages come from _tensor), and the device
+# switched only when it is not the current one.
+
+
+def _i8_ptr(t, dtype, shape, name):
+    """The address of a contiguous CUDA tensor of the given type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    _tensor(t, dtype, len(shape), name)
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _i8_conv_dtype(t, name):
     """The conv_dtype of a bfloat16 or float32 tensor."""
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype == torch.bfloat16:
-        return CONV_BF16
-    if t.dtype == torch.float32:
-        return CONV_F32
-    raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if isinstance(t, torch.Tensor):
+        if t.dtype is torch.bfloat16:
+            return CONV_BF16
+        if t.dtype is torch.float32:
+            return CONV_F32
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    raise TypeError(f"{name} must be a torch.Tensor")
 
 
-def empty_rows_i8(rows, C, device="cuda"):
-    """An uninitialised int8 matrix [rows, C] in the layout the 8-bit operators take: rows start
-    on 16-byte boundaries, so the tensor is a view of [rows, pitch] where C is not a multiple of
-    16. Copy 8-bit rows from elsewhere (a checkpoint's filter) into one with copy_()."""
-    import torch
-    pitch = lib.conv_i8_row_pitch(int(C))
-    if pitch == 0 or rows < 1:
-        raise ValueError("rows and C must be positive")
-    return torch.empty((rows, pitch), dtype=torch.int8, device=device)[:, :C]
-
-
-def _rows_i8(t, name, rows=None, C=None):
-    """(pointer, row pitch) of an int8 matrix whose rows start on 16-byte boundaries."""
+def _i8_rows(t, name, rows=None, C=None):
+    """(address, row pitch) of an int8 matrix whose rows start on 16-byte boundaries."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int8:
+    if t.dtype is not torch.int8:
         raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -442,35 +445,68 @@ def _rows_i8(t, name, rows=None, C=None):
         raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
     n, c = t.shape
     if (rows is not None and n != rows) or (C is not None and c != C):
-        raise ValueError(f"{name} has the wrong shape")
-    # the stride of a dimension with one element means nothing
-    pitch = t.stride(0) if n > 1 else (c + 15) // 16 * 16
-    if (c > 1 and t.stride(1) != 1) or pitch < c or pitch % 16:
+        raise ValueError(f"{name} must have shape {(rows if rows is not None else n, C if C is not None else c)}, got {(n, c)}")
+    pitch, step = t.stride()
+    if n < 2:
+        pitch = (c + 15) // 16 * 16   # the stride of a dimension with one element means nothing
+    if (step != 1 and c > 1) or pitch < c or pitch & 15:
         raise ValueError(f"{name} must be an int8 matrix whose rows are contiguous and start on 16-byte boundaries "
                          "(empty_rows_i8 makes one)")
     return t.data_ptr(), pitch
 
 
-def _scales(t, n, name):
-    p = _tensor(t, _f32(), 1, name)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries")
-    return p
-
-
-def _f32():
+def _i8_call(fn, what, tensors, stream, *args):
+    """_call for the 8-bit entry points."""
     import torch
-    return torch.float32
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            _device(*tensors)
+    if stream is None and index == torch._C._cuda_getDevice():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        if rc != CONV_OK:
+            _check(rc, what)
+    else:
+        _call(fn, what, tensors, stream, *args)
 
 
-def _new_rows_i8(q, scale, rows, C, device):
-    """q and scale, allocated where None."""
+def empty_rows_i8(rows, C, device="cuda"):
+    """An uninitialised int8 matrix [rows, C] in the layout the 8-bit operators take, a view of
+    [rows, pitch] whose rows start where conv_i8_row_pitch puts them. Copy 8-bit rows from
+    elsewhere (a checkpoint's filter) into one with copy_()."""
+    import torch
+    pitch = lib.conv_i8_row_pitch(int(C))
+    if pitch == 0 or rows < 1:
+        raise ValueError("rows and C must be positive")
+    return torch.empty((rows, pitch), dtype=torch.int8, device=device)[:, :C]
+
+
+def _i8_out(q, scale, rows, C, device):
+    """q and scale (allocated where None), their addresses and q's pitch."""
     import torch
     if q is None:
         q = empty_rows_i8(rows, C, device)
     if scale is None:
         scale = torch.empty(rows, dtype=torch.float32, device=device)
-    return q, scale
+    pq, pitch = _i8_rows(q, "q", rows, C)
+    return q, scale, pq, pitch, _i8_ptr(scale, torch.float32, (rows,), "scale")
+
+
+def _i8_result(y, dtype, shape, device):
+    import torch
+    if y is None:
+        return torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+    if dtype is not None and y.dtype is not dtype:
+        raise TypeError(f"y must be {dtype}, got {y.dtype}")
+    return y
+
+
+def _i8_matrix(x, name):
+    """(conv_dtype, address) of a contiguous bfloat16 or float32 CUDA matrix."""
+    dt = _i8_conv_dtype(x, name)
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        _tensor(x, x.dtype, 2, name)
+    return dt, x.data_ptr()
 
 
 def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-6, stream=None):
@@ -480,97 +516,79 @@ def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-
     weight is float32 [C]. h may be x or residual (updated in place). Returns (q, scale, h); h is
     None without a residual."""
     import torch
-    dt = _i8_dtype(x, "x")
-    px = _tensor(x, x.dtype, 2, "x")
+    dt, px = _i8_matrix(x, "x")
     M, C = x.shape
-    pw = _scales(weight, C, "weight")
+    pw = _i8_ptr(weight, torch.float32, (C,), "weight")
     pr = ph = None
     if residual is not None:
-        pr = _tensor(residual, x.dtype, 2, "residual")
-        if residual.shape != x.shape:
-            raise ValueError("residual must have x's shape")
+        pr = _i8_ptr(residual, x.dtype, x.shape, "residual")
         if h is None:
             h = torch.empty_like(x)
-        elif h.shape != x.shape:
-            raise ValueError("h has the wrong shape")
-        ph = _tensor(h, x.dtype, 2, "h")
+        ph = _i8_ptr(h, x.dtype, x.shape, "h")
     elif h is not None:
         raise ValueError("h is x + residual: give the residual too")
-    q, scale = _new_rows_i8(q, scale, M, C, x.device)
-    pq, ldq = _rows_i8(q, "q", M, C)
-    ps = _scales(scale, M, "scale")
-    _call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", (x, residual, weight, h, q, scale), stream,
-          px, pr, pw, ph, pq, ps, M, C, ldq, float(eps), dt)
+    q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
+    _i8_call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", (x, residual, weight, h, q, scale), stream,
+             px, pr, pw, ph, pq, ps, M, C, ldq, eps, dt)
     return q, scale, h
 
 
 def quant_rows_i8_fwd(x, glu=False, q=None, scale=None, stream=None):
     """8-bit rows of x [M, C] (bfloat16 or float32): int8 q [M, C] and float32 scale [M], one per row.
     With glu, x is [M, 2C] and the rows are silu(x[:, :C]) * x[:, C:]. Returns (q, scale)."""
-    dt = _i8_dtype(x, "x")
-    px = _tensor(x, x.dtype, 2, "x")
+    dt, px = _i8_matrix(x, "x")
     M, C = x.shape
     if glu:
         if C % 2:
             raise ValueError("glu needs x [M, 2C]")
         C //= 2
-    q, scale = _new_rows_i8(q, scale, M, C, x.device)
-    pq, ldq = _rows_i8(q, "q", M, C)
-    ps = _scales(scale, M, "scale")
-    _call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", (x, q, scale), stream, px, pq, ps, M, C, ldq, 1 if glu else 0, dt)
+    q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
+    _i8_call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", (x, q, scale), stream, px, pq, ps, M, C, ldq, 1 if glu else 0, dt)
     return q, scale
 
 
 def quant_filter_i8_fwd(F, q=None, scale=None, stream=None):
     """8-bit rows of a 1 x 1 filter F [Cin, Cout] or [1, 1, Cin, Cout] (bfloat16 or float32): int8
     q [Cout, Cin], transposed, and float32 scale [Cout], one per output channel. Returns (q, scale)."""
-    dt = _i8_dtype(F, "F")
+    dt = _i8_conv_dtype(F, "F")
     if F.dim() == 4 and tuple(F.shape[:2]) != (1, 1):
         raise ValueError("F must be a 1 x 1 filter")
     pf = _tensor(F, F.dtype, 4 if F.dim() == 4 else 2, "F")
     Cin, Cout = F.shape[-2:]
-    q, scale = _new_rows_i8(q, scale, Cout, Cin, F.device)
-    pq, ldw = _rows_i8(q, "q", Cout, Cin)
-    ps = _scales(scale, Cout, "scale")
-    _call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", (F, q, scale), stream, pf, pq, ps, Cin, Cout, ldw, dt)
+    q, scale, pq, ldw, ps = _i8_out(q, scale, Cout, Cin, F.device)
+    _i8_call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", (F, q, scale), stream, pf, pq, ps, Cin, Cout, ldw, dt)
     return q, scale
 
 
 def dequant_rows_i8_fwd(q, scale, y=None, dtype=None, stream=None):
     """Reads 8-bit rows back: y [M, C] = q * scale, in y's type (dtype, bfloat16 by default)."""
-    pq, ldq = _rows_i8(q, "q")
-    M, C = q.shape
-    ps = _scales(scale, M, "scale")
-    y = _output(y, dtype, (M, C), q.device)
-    dt = _i8_dtype(y, "y")
-    py = _tensor(y, y.dtype, 2, "y")
-    _call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", (q, scale, y), stream, pq, ps, py, M, C, ldq, dt)
-    return y
-
-
-def _output(y, dtype, shape, device):
     import torch
-    if y is None:
-        return torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
-    if tuple(y.shape) != shape or (dtype is not None and y.dtype != dtype):
-        raise ValueError("y has the wrong shape or type")
+    pq, ldq = _i8_rows(q, "q")
+    M, C = q.shape
+    ps = _i8_ptr(scale, torch.float32, (M,), "scale")
+    y = _i8_result(y, dtype, (M, C), q.device)
+    dt = _i8_conv_dtype(y, "y")
+    py = _i8_ptr(y, y.dtype, (M, C), "y")
+    _i8_call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", (q, scale, y), stream, pq, ps, py, M, C, ldq, dt)
     return y
 
 
 def pointwise_i8_fwd(q, q_scale, Wq, w_scale, bias=None, y=None, dtype=None, stream=None):
     """The product of 8-bit rows: y [M, Cout] = (q [M, Cin] @ Wq [Cout, Cin]^T) * q_scale [M] * w_scale [Cout]
     + bias [Cout], the sum exact in int32, in y's type (dtype, bfloat16 by default)."""
-    pq, ldq = _rows_i8(q, "q")
+    import torch
+    pq, ldq = _i8_rows(q, "q")
     M, Cin = q.shape
-    pw, ldw = _rows_i8(Wq, "Wq", None, Cin)
+    pw, ldw = _i8_rows(Wq, "Wq", None, Cin)
     Cout = Wq.shape[0]
-    ps, pws = _scales(q_scale, M, "q_scale"), _scales(w_scale, Cout, "w_scale")
-    pb = None if bias is None else _scales(bias, Cout, "bias")
-    y = _output(y, dtype, (M, Cout), q.device)
-    dt = _i8_dtype(y, "y")
-    py = _tensor(y, y.dtype, 2, "y")
-    _call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", (q, q_scale, Wq, w_scale, bias, y), stream,
-          pq, ps, pw, pws, pb, py, M, Cin, Cout, ldq, ldw, dt)
+    f32 = torch.float32
+    ps, pws = _i8_ptr(q_scale, f32, (M,), "q_scale"), _i8_ptr(w_scale, f32, (Cout,), "w_scale")
+    pb = None if bias is None else _i8_ptr(bias, f32, (Cout,), "bias")
+    y = _i8_result(y, dtype, (M, Cout), q.device)
+    dt = _i8_conv_dtype(y, "y")
+    py = _i8_ptr(y, y.dtype, (M, Cout), "y")
+    _i8_call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", (q, q_scale, Wq, w_scale, bias, y), stream,
+             pq, ps, pw, pws, pb, py, M, Cin, Cout, ldq, ldw, dt)
     return y
 
 
@@ -582,11 +600,12 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
     import torch
     px = _tensor(X, torch.bfloat16, 4, "X")
     N, H, W, Cin = X.shape
-    pw, ldw = _rows_i8(Wq, "Wq", None, Cin)
+    pw, ldw = _i8_rows(Wq, "Wq", None, Cin)
     Cout = Wq.shape[0]
-    pws = _scales(w_scale, Cout, "w_scale")
-    pb = None if bias is None else _scales(bias, Cout, "bias")
-    pn = None if norm is None else _scales(norm, Cin, "norm")
+    f32 = torch.float32
+    pws = _i8_ptr(w_scale, f32, (Cout,), "w_scale")
+    pb = None if bias is None else _i8_ptr(bias, f32, (Cout,), "bias")
+    pn = None if norm is None else _i8_ptr(norm, f32, (Cin,), "norm")
     if workspace is None:
         need = lib.conv2d_nhwc_i8_workspace(N, H, W, Cin)
         if need == 0:
@@ -596,12 +615,10 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if Y is None:
         Y = torch.empty((N, H, W, Cout), dtype=torch.bfloat16, device=X.device)
-    elif tuple(Y.shape) != (N, H, W, Cout):
-        raise ValueError("Y has the wrong shape")
-    py = _tensor(Y, torch.bfloat16, 4, "Y")
-    _call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", (X, norm, Wq, w_scale, bias, Y, workspace), stream,
-          px, pn, float(eps), pw, pws, pb, py, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-          N, H, W, Cin, Cout, ldw)
+    py = _i8_ptr(Y, torch.bfloat16, (N, H, W, Cout), "Y")
+    _i8_call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", (X, norm, Wq, w_scale, bias, Y, workspace), stream,
+             px, pn, eps, pw, pws, pb, py, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+             N, H, W, Cin, Cout, ldw)
     return Y
 
 

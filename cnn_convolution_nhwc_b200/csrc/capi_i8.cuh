@@ -19,35 +19,31 @@ int check_i8_rows(const void *q, int C, int ld) {
 }
 
 // ---- rows ------------------------------------------------------------------------------
-template <typename T, int MODE, int NV, bool VEC, bool GROUP_WARP, bool STREAM>
+template <typename T, int MODE, int NV, bool VEC, int TPR, bool STREAM>
 int launch_i8_rows(const I8RowsParams &p, int threads, cudaStream_t stream, DeviceState *d) {
-    const long long per = GROUP_WARP ? threads / 32 : 1, blocks = (p.M + per - 1) / per;
+    const long long per = TPR == 32 ? threads / 32 : 1, blocks = (p.M + per - 1) / per;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = stream;
-    return launched(launch_k(cfg, i8_rows_kernel<T, MODE, NV, VEC, GROUP_WARP, STREAM>, p, d->status), "i8_rows_kernel");
+    return launched(launch_k(cfg, i8_rows_kernel<T, MODE, NV, VEC, TPR, STREAM>, p, d->status), "i8_rows_kernel");
 }
 
 template <typename T, int MODE>
 int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
+    // A warp holds rows up to 1024 values, a block of up to 512 threads rows up to 16384.
     const int C = p.C;
-    const bool vec = C % 8 == 0 && aligned(p.x, 16) && (!p.residual || aligned(p.residual, 16)) &&
-                     (!p.h || aligned(p.h, 16)) && (!p.weight || aligned(p.weight, 16));
-    auto block = [&](int nv) {   // threads of a block that holds a row, nv groups of eight a thread
-        const int t = ((C + 8 * nv - 1) / (8 * nv) + 31) / 32 * 32;
-        return t < 512 ? t : 512;
-    };
-    if (vec) {
-        if (C <= 512) return launch_i8_rows<T, MODE, 2, true, true, false>(p, 256, stream, d);
-        if (C <= 1024) return launch_i8_rows<T, MODE, 4, true, true, false>(p, 256, stream, d);
-        if (C <= 8192) return launch_i8_rows<T, MODE, 2, true, false, false>(p, block(2), stream, d);
-        if (C <= 16384) return launch_i8_rows<T, MODE, 4, true, false, false>(p, block(4), stream, d);
-        return launch_i8_rows<T, MODE, 4, true, false, true>(p, 512, stream, d);
+    if (C % 8 == 0 && aligned(p.x, 16) && aligned(p.residual, 16) && aligned(p.h, 16) && aligned(p.weight, 16)) {
+        if (C <= 512) return launch_i8_rows<T, MODE, 2, true, 32, false>(p, 128, stream, d);
+        if (C <= 1024) return launch_i8_rows<T, MODE, 4, true, 32, false>(p, 128, stream, d);
+        if (C <= 16384) return launch_i8_rows<T, MODE, 4, true, 0, false>(p, (C + 1023) / 1024 * 32, stream, d);
+        return launch_i8_rows<T, MODE, 4, true, 0, true>(p, 512, stream, d);
     }
-    if (C <= 1024) return launch_i8_rows<T, MODE, 4, false, true, false>(p, 256, stream, d);
-    if (C <= 16384) return launch_i8_rows<T, MODE, 4, false, false, false>(p, block(4), stream, d);
-    return launch_i8_rows<T, MODE, 4, false, false, true>(p, 512, stream, d);
+    if (C <= 512) return launch_i8_rows<T, MODE, 2, false, 32, false>(p, 128, stream, d);
+    if (C <= 2048) return launch_i8_rows<T, MODE, 2, false, 128, false>(p, 128, stream, d);
+    if (C <= 4096) return launch_i8_rows<T, MODE, 2, false, 256, false>(p, 256, stream, d);
+    if (C <= 8192) return launch_i8_rows<T, MODE, 2, false, 512, false>(p, 512, stream, d);
+    return launch_i8_rows<T, MODE, 2, false, 512, true>(p, 512, stream, d);
 }
 
 template <int MODE>
@@ -56,15 +52,16 @@ int run_i8_rows(const I8RowsParams &p, int dtype, cudaStream_t stream, DeviceSta
 }
 
 // ---- product -----------------------------------------------------------------------------
-// A matrix of 8-bit rows: boxes of 128 values x `box_rows` rows, 128-byte swizzle.
-int i8_map(CUtensorMap *m, const int8_t *q, int rows, int C, int ld, int box_rows) {
-    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld};
-    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return g_encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t *>(q), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+// A matrix of 8-bit rows in boxes of 128 values x `box_rows` rows, 128-byte swizzle; with kb > 1 the
+// values are split into blocks of 128 (C a multiple of 128) and a box has kb of them.
+int i8_map(CUtensorMap *m, const int8_t *q, int rows, int C, int ld, int box_rows, int kb = 1) {
+    const cuuint64_t dims[3] = {kb > 1 ? 128u : (cuuint64_t)C, (cuuint64_t)rows, (cuuint64_t)C / 128};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld, 128};
+    const cuuint32_t box[3] = {128, (cuuint32_t)box_rows, (cuuint32_t)kb};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return g_encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, kb > 1 ? 3 : 2, const_cast<int8_t *>(q), dims, strides, box,
+                          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? CONV_OK
                : CONV_ERR_CUDA;
 }
@@ -79,11 +76,14 @@ int launch_i8_split(const I8Operands &a, I8GemmParams p, int split, cudaStream_t
     auto kern = i8_split_kernel<Cfg, OUT>;
     if (int rc = ensure_smem_attr(d, bit, kern, Cfg::SMEM)) return rc;
     CUtensorMap tmW, tmQ;
-    if (int rc = i8_map(&tmW, a.Wq, p.N, a.Cin, a.ldw, 128)) return rc;
-    if (int rc = i8_map(&tmQ, a.q, p.M, a.Cin, a.ldq, Cfg::BN)) return rc;
+    p.wide = Cfg::KB > 1 && a.Cin % 128 == 0;
+    if (int rc = i8_map(&tmW, a.Wq, p.N, a.Cin, a.ldw, 128, p.wide ? Cfg::KB : 1)) return rc;
+    if (int rc = i8_map(&tmQ, a.q, p.M, a.Cin, a.ldq, Cfg::BN, p.wide ? Cfg::KB : 1)) return rc;
     p.n_tiles = (p.N + 127) / 128;
     p.m_tiles = (p.M + Cfg::BN - 1) / Cfg::BN;
     p.split = split;
+    p.own_shift = 0;
+    while ((Cfg::BN >> (p.own_shift + 1)) >= split) ++p.own_shift;   // BN / split, powers of two
     const long long ctas = 1LL * p.n_tiles * p.m_tiles * split;
     if (ctas > kInt32Max) return CONV_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
@@ -103,16 +103,27 @@ int launch_i8_split(const I8Operands &a, I8GemmParams p, int split, cudaStream_t
     return launched(launch_k(cfg, kern, tmW, tmQ, p, d->status), "i8_split_kernel");
 }
 
-template <typename OUT>
+template <class Cfg, typename OUT>
 int launch_i8_pair(const I8Operands &a, I8GemmParams p, cudaStream_t stream, DeviceState *d, unsigned bit) {
-    using Cfg = I8PairCfg;
-    auto kern = i8_pair_kernel<OUT>;
+    auto kern = i8_pair_kernel<Cfg, OUT>;
     if (int rc = ensure_smem_attr(d, bit, kern, Cfg::SMEM)) return rc;
-    CUtensorMap tmQ, tmW;
+    CUtensorMap tmQ, tmW, tmY;
     if (int rc = i8_map(&tmQ, a.q, p.M, a.Cin, a.ldq, 128)) return rc;
-    if (int rc = i8_map(&tmW, a.Wq, p.N, a.Cin, a.ldw, 128)) return rc;
+    if (int rc = i8_map(&tmW, a.Wq, p.N, a.Cin, a.ldw, Cfg::BN / 2)) return rc;
+    if (p.vec) {   // Y in boxes of 32 rows x 128 bytes
+        const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
+        const cuuint64_t strides[1] = {(cuuint64_t)p.N * sizeof(OUT)};
+        const cuuint32_t box[2] = {128 / (cuuint32_t)sizeof(OUT), 32};
+        const cuuint32_t estr[2] = {1, 1};
+        if (g_encode_tiled(&tmY, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                           p.Y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return CONV_ERR_CUDA;
+    } else {
+        tmY = tmQ;   // not used
+    }
     p.m_tiles = (p.M + 255) / 256;
-    p.n_tiles = (p.N + 255) / 256;
+    p.n_tiles = (p.N + Cfg::BN - 1) / Cfg::BN;
     p.split = 1;
     const long long tiles = 1LL * p.m_tiles * p.n_tiles;
     if (tiles > kInt32Max / 2) return CONV_ERR_UNSUPPORTED;
@@ -132,29 +143,35 @@ int launch_i8_pair(const I8Operands &a, I8GemmParams p, cudaStream_t stream, Dev
     cfg.blockDim = dim3(Cfg::THREADS);
     cfg.dynamicSmemBytes = Cfg::SMEM;
     cfg.stream = stream;
-    return launched(launch_k(cfg, kern, tmQ, tmW, p, d->status), "i8_pair_kernel");
+    return launched(launch_k(cfg, kern, tmQ, tmW, tmY, p, d->status), "i8_pair_kernel");
 }
 
-// The kernel for a product: bn = 0 for the pair kernel, else the split kernel's token columns, and
-// its split of the reduction.
+// The kernel for a product: the pair kernel's tile width, or the split kernel's token columns and its
+// split of the reduction.
 struct I8Plan {
+    bool pair;
     int bn, split;
 };
 
 I8Plan plan_i8(int M, int N, int num_kblk, int num_sms) {
-    I8Plan pl{0, 1};
-    if (M <= 512) {
+    I8Plan pl{true, 256, 1};
+    if (M <= 128) {
+        pl.pair = false;
         pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
         const long long tiles = 1LL * ((N + 127) / 128) * ((M + pl.bn - 1) / pl.bn);
         while (pl.split < 8 && tiles * pl.split * 2 <= num_sms && pl.split * 4 <= num_kblk) pl.split *= 2;
+    } else {
+        // half-width tiles while whole ones would leave half of the pairs idle
+        const long long tiles = 1LL * ((M + 255) / 256) * ((N + 255) / 256);
+        if (tiles * 4 <= num_sms) pl.bn = 128;
     }
-    // CONV_B200_I8 (tests): "pair", or "split,BN,S"
+    // CONV_B200_I8 (tests): "pair,BN", or "split,BN,S"
     if (const char *f = env("CONV_B200_I8")) {
         int bn = 0, s = 0;
-        if (std::strcmp(f, "pair") == 0) pl = I8Plan{0, 1};
+        if (std::sscanf(f, "pair,%d", &bn) == 1 && (bn == 128 || bn == 256)) pl = I8Plan{true, bn, 1};
         else if (std::sscanf(f, "split,%d,%d", &bn, &s) == 2 && (bn == 16 || bn == 32 || bn == 64 || bn == 128) &&
-                 (s == 1 || s == 2 || s == 4 || s == 8) && s <= num_kblk)
-            pl = I8Plan{bn, s};
+                 (s == 1 || s == 2 || s == 4 || s == 8) && s <= (num_kblk + 1) / 2)
+            pl = I8Plan{false, bn, s};
     }
     return pl;
 }
@@ -164,13 +181,22 @@ int run_i8_product(const I8Operands &a, I8GemmParams p, cudaStream_t stream, Dev
     p.num_kblk = (a.Cin + 127) / 128;
     p.vec = aligned(p.Y, 16) && (1LL * p.N * sizeof(OUT)) % 16 == 0;
     const I8Plan pl = plan_i8(p.M, p.N, p.num_kblk, d->num_sms);
-    constexpr unsigned bit = sizeof(OUT) == 4 ? 116 : 112;
+    constexpr unsigned bit = sizeof(OUT) == 4 ? 120 : 112;
+    if (pl.pair)
+        return pl.bn == 256 ? launch_i8_pair<I8PairCfg<256, 5>, OUT>(a, p, stream, d, bit)
+                            : launch_i8_pair<I8PairCfg<128, 7>, OUT>(a, p, stream, d, bit + 1);
+    // one CTA per SM has the whole shared memory for copies in flight; with more, two share an SM
+    const long long ctas = 1LL * ((p.N + 127) / 128) * ((p.M + pl.bn - 1) / pl.bn) * pl.split;
+    const bool deep = ctas <= d->num_sms;
     switch (pl.bn) {
-        case 16: return launch_i8_split<I8SplitCfg<16, 5>, OUT>(a, p, pl.split, stream, d, bit);
-        case 32: return launch_i8_split<I8SplitCfg<32, 4>, OUT>(a, p, pl.split, stream, d, bit + 1);
-        case 64: return launch_i8_split<I8SplitCfg<64, 3>, OUT>(a, p, pl.split, stream, d, bit + 2);
-        case 128: return launch_i8_split<I8SplitCfg<128, 4>, OUT>(a, p, pl.split, stream, d, bit + 3);
-        default: return launch_i8_pair<OUT>(a, p, stream, d, sizeof(OUT) == 4 ? 121 : 120);
+        case 16:
+            return deep ? launch_i8_split<I8SplitCfg<16, 6, 2>, OUT>(a, p, pl.split, stream, d, bit + 2)
+                        : launch_i8_split<I8SplitCfg<16, 5, 1>, OUT>(a, p, pl.split, stream, d, bit + 3);
+        case 32:
+            return deep ? launch_i8_split<I8SplitCfg<32, 5, 2>, OUT>(a, p, pl.split, stream, d, bit + 4)
+                        : launch_i8_split<I8SplitCfg<32, 4, 1>, OUT>(a, p, pl.split, stream, d, bit + 5);
+        case 64: return launch_i8_split<I8SplitCfg<64, 4, 2>, OUT>(a, p, pl.split, stream, d, bit + 6);
+        default: return launch_i8_split<I8SplitCfg<128, 5, 1>, OUT>(a, p, pl.split, stream, d, bit + 7);
     }
 }
 
@@ -313,12 +339,16 @@ int dequant_rows_i8_fwd(const int8_t *q, const float *scale, void *y, int M, int
     DeviceState *d = nullptr;
     if (int rc = device_state(&d)) return rc;
     if (int rc = check_device_ptrs(stream, {q, scale, y})) return rc;
-    I8DequantParams p{q, scale, y, M, C, ldq, (C + 511) / 512};
-    const long long blocks = (1LL * M * p.segs + 7) / 8;
-    if (blocks > kInt32Max) return CONV_ERR_UNSUPPORTED;
-    const bool vec = C % 16 == 0 && aligned(y, 16);
+    I8DequantParams p{q, scale, y, M, C, ldq, 0};
+    const bool vec = (1LL * C * e) % 16 == 0 && aligned(y, 16);
+    const int seg = vec ? 4 * 32 * (16 / e) : 512;   // values a warp takes
+    const int segs = (C + seg - 1) / seg;
+    while (p.wpr_shift < 3 && (1 << p.wpr_shift) < segs) ++p.wpr_shift;
+    const long long blocks = (1LL * M + (8 >> p.wpr_shift) - 1) >> (3 - p.wpr_shift);
+    const long long seg_blocks = (segs + (1 << p.wpr_shift) - 1) >> p.wpr_shift;
+    if (blocks > kInt32Max || seg_blocks > 65535) return CONV_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(seg_blocks));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaError_t rc;

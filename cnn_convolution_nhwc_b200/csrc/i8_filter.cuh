@@ -50,7 +50,12 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
         if (c >= c1) return;
         const long long at = 1LL * c * p.Cout + o0 + cg;
         if constexpr (VEC) {
-            if (o0 + cg < p.Cout && in_bounds(at, 8, f_elems, kSiteI8FilterF, status)) i8_load8(F + at, v);
+            if (o0 + cg < p.Cout && in_bounds(at, 8, f_elems, kSiteI8FilterF, status)) {
+                uint64_t t[4];
+                i8_unpack(i8_raw_load(F + at), t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f2_split(t[i], v[2 * i], v[2 * i + 1]);
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -140,45 +145,74 @@ struct I8DequantParams {
     void *y;               // [M][C]
     long long M;
     int C, ldq;
-    int segs;              // ceil(C / 512): warps per row
+    int wpr_shift;         // log2 of the warps of a block that share a row
 };
 
 __device__ __forceinline__ void i8_put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void i8_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// y = q * scale, one rounding. A warp takes 512 values of a row: 16 neighbours a lane (VEC: C a
-// multiple of 16 and y 16-byte aligned), or one of every 32.
+// y = q * scale, one rounding. A warp takes a segment of a row, four accesses a lane in flight: 16
+// bytes of y each (VEC: rows of y on 16 bytes), so that the warp's stores are whole lines; else 16
+// values a lane, one of every 32. blockIdx.y counts the segments that do not fit in one block.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256)
 i8_dequant_kernel(const I8DequantParams p, unsigned int *status) {
     grid_dependents_launch();
     grid_dependency_wait();
-    const int lane = threadIdx.x & 31;
-    const long long job = 8LL * blockIdx.x + (threadIdx.x >> 5);
-    const long long row = job / p.segs;
-    if (row >= p.M) return;
-    const int c0 = static_cast<int>(job - row * p.segs) * 512;
-    const float s = p.scale[row];
+    constexpr int PER = 16 / sizeof(T);   // values of a 16-byte store
+    constexpr int SEG = VEC ? 4 * 32 * PER : 512;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long row = (static_cast<long long>(blockIdx.x) << (3 - p.wpr_shift)) + (warp >> p.wpr_shift);
+    const long long start = ((static_cast<long long>(blockIdx.y) << p.wpr_shift) + (warp & ((1 << p.wpr_shift) - 1))) * SEG;
+    if (row >= p.M || start >= p.C) return;
+    const int c0 = static_cast<int>(start);
     const int8_t *q = p.q + row * p.ldq;
     T *y = static_cast<T *>(p.y) + row * p.C;
     const long long elems = p.M * p.C;
+    const float s = p.scale[row];
     if constexpr (VEC) {
-        const int c = c0 + lane * 16;
-        if (c >= p.C || !in_bounds(row * p.C + c, 16, elems, kSiteI8Dequant, status)) return;
-        const uint4 u = *reinterpret_cast<const uint4 *>(q + c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        float v[2][8];
+        uint2 w[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            v[i >> 3][i & 7] = i8_round_to(static_cast<float>(static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)))) * s, T());
-        i8_store8(y + c, v[0]);
-        i8_store8(y + c + 8, v[1]);
+        for (int k = 0; k < 4; ++k) {
+            const int c = c0 + (k * 32 + lane) * PER;
+            w[k] = make_uint2(0u, 0u);
+            if (c < p.C) {
+                if constexpr (PER == 8) w[k] = *reinterpret_cast<const uint2 *>(q + c);
+                else w[k].x = *reinterpret_cast<const uint32_t *>(q + c);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int c = c0 + (k * 32 + lane) * PER;
+            if (c >= p.C || !in_bounds(row * p.C + c, PER, elems, kSiteI8Dequant, status)) continue;
+            uint32_t out[4];
+#pragma unroll
+            for (int i = 0; i < PER / 2; ++i) {
+                const uint32_t u = (i < 2 ? w[k].x : w[k].y) >> (16 * (i & 1));
+                float lo, hi;
+                f2_split(f2_mul(f2_pack(static_cast<float>(static_cast<int8_t>(u)), static_cast<float>(static_cast<int8_t>(u >> 8))),
+                                f2_pack(s, s)), lo, hi);
+                if constexpr (PER == 8) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+                    out[i] = *reinterpret_cast<const uint32_t *>(&v);
+                } else {
+                    out[2 * i] = __float_as_uint(lo);
+                    out[2 * i + 1] = __float_as_uint(hi);
+                }
+            }
+            *reinterpret_cast<uint4 *>(y + c) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
     } else {
+        int8_t v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int c = c0 + i * 32 + lane;
-            if (c < p.C && in_bounds(row * p.C + c, 1, elems, kSiteI8Dequant, status))
-                i8_put(y + c, static_cast<float>(q[c]) * s);
+            v[i] = c < p.C ? q[c] : static_cast<int8_t>(0);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int c = c0 + i * 32 + lane;
+            if (c < p.C && in_bounds(row * p.C + c, 1, elems, kSiteI8Dequant, status)) i8_put(y + c, static_cast<float>(v[i]) * s);
         }
     }
 }

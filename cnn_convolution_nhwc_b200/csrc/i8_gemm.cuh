@@ -13,6 +13,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include "dense_tc.cuh"
 #include "dense_halo.cuh"
 #include "i8_rows.cuh"
 #include "ptx.cuh"
@@ -28,9 +29,16 @@ struct I8GemmParams {
     int num_kblk;           // ceil(Cin / 128)
     int n_tiles;            // tiles along N
     int m_tiles;            // tiles along M
-    int split;              // CTAs per cluster, each with its share of the k blocks (split kernel)
+    int split;              // split kernel: CTAs per cluster, each with its share of the k blocks
+    int wide;               // split kernel: slots of several k blocks in one copy (Cin a multiple of 128)
+    int own_shift;          // split kernel: log2 of the token columns a CTA of a cluster owns
     int num_tiles;
     int vec;                // 16-byte stores: rows of Y on 16-byte boundaries
+};
+
+template <int N>
+struct I8Int {
+    static constexpr int value = N;
 };
 
 __device__ __forceinline__ void i8_out(float *p, float v) { *p = v; }
@@ -43,19 +51,23 @@ __device__ __forceinline__ void i8_out(__nv_bfloat16 *p, float v) { *p = __float
 // accumulates its share in TMEM, sends each token column to the CTA of the cluster that owns it
 // (distributed shared memory), and after one cluster barrier the owners add the shares, which are
 // integers: the result does not depend on the split.
-//   warp 0      TMA: one slot (128 filter rows and BN token rows of 128 bytes) per k block
+//   warp 0      TMA: slots of KB k blocks of 128 filter rows and BN token rows. A copy costs its
+//               issuing warp 0.08 us whatever its size, so a slot of two k blocks is two copies of
+//               3-D boxes (128 values, rows, k blocks) where Cin is a multiple of 128; elsewhere
+//               a k block each, whose extent ends at Cin (p.wide).
 //   warp 1      TMEM allocation, MMA issue (M = 128, N = BN)
-//   warps 2..5  epilogue, one TMEM lane quarter each
-template <int BN_, int STAGES_>
+//   warps 2..9  epilogue, two warps per TMEM lane quarter taking alternate groups of 16 tokens
+template <int BN_, int STAGES_, int KB_>
 struct I8SplitCfg {
-    static constexpr int BN = BN_, STAGES = STAGES_;
-    static constexpr int W_BYTES = 128 * 128, Q_BYTES = BN * 128;
+    static constexpr int BN = BN_, STAGES = STAGES_, KB = KB_;
+    static constexpr int W_BYTES = KB * 128 * 128, Q_BYTES = KB * BN * 128;
     static constexpr int SLOT = W_BYTES + Q_BYTES;
     static constexpr int RECV_BYTES = BN * 128 * 4;   // the owned columns' shares: split x (BN / split) x 128
     static constexpr int TMEM_COLS = BN < 32 ? 32 : BN;
     static constexpr int SMEM = 1024 + STAGES * SLOT + RECV_BYTES + BN * 4 + (2 * STAGES + 1) * 8 + 16;
-    static constexpr int THREADS = 192;
+    static constexpr int THREADS = 320;
     static constexpr uint32_t IDESC = idesc_i8_s32(128, BN);
+    static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
 template <class Cfg, typename OUT>
@@ -63,7 +75,7 @@ __global__ void __launch_bounds__(Cfg::THREADS)
 i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmQ, const I8GemmParams p,
                 unsigned int *status) {
     grid_dependents_launch();
-    constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES;
+    constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, KB = Cfg::KB;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
@@ -83,9 +95,9 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const int tile = static_cast<int>(blockIdx.x / S);
     const int mt = tile / p.n_tiles;
     const int n0 = (tile - mt * p.n_tiles) * 128, m0 = mt * BN;
-    const int kb0 = static_cast<int>(1LL * p.num_kblk * rank / S), kb1 = static_cast<int>(1LL * p.num_kblk * (rank + 1) / S);
+    const int num_sb = (p.num_kblk + KB - 1) / KB;   // slots of the whole reduction, and this CTA's share
+    const int sb0 = static_cast<int>(1LL * num_sb * rank / S), sb1 = static_cast<int>(1LL * num_sb * (rank + 1) / S);
     const int cols = p.M - m0 < BN ? p.M - m0 : BN;   // tokens of this tile
-    const int own = BN / static_cast<int>(S);         // columns a CTA of the cluster owns
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -111,18 +123,24 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     grid_dependency_wait();
 
     if (warp == 0) {
+        const uint32_t leader = elect_one_sync();
         bool ok = true;
         uint32_t s = 0, ph = 0;
         int issued = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int sb = sb0; sb < sb1; ++sb) {
             if (!mbar_wait_warp(empty(s), ph ^ 1u)) { ok = false; break; }
-            if (lane == 0) {
-                const uint32_t slot = base + s * Cfg::SLOT;
-                mbar_arrive_expect_tx(full(s), Cfg::SLOT);
-                tma_load_2d(slot, &tmW, full(s), kb * 128, n0);
-                tma_load_2d(slot + Cfg::W_BYTES, &tmQ, full(s), kb * 128, m0);
+            const uint32_t slot = base + s * Cfg::SLOT;
+            mbar_arrive_expect_tx_if(full(s), Cfg::SLOT, leader);
+            if (KB > 1 && p.wide) {
+                tma_load_3d_if(slot, &tmW, full(s), 0, n0, sb * KB, leader);
+                tma_load_3d_if(slot + Cfg::W_BYTES, &tmQ, full(s), 0, m0, sb * KB, leader);
+            } else {
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    tma_load_2d_if(slot + b * 128 * 128, &tmW, full(s), (sb * KB + b) * 128, n0, leader);
+                    tma_load_2d_if(slot + Cfg::W_BYTES + b * BN * 128, &tmQ, full(s), (sb * KB + b) * 128, m0, leader);
+                }
             }
-            __syncwarp();
             ++issued;
             if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
@@ -137,14 +155,15 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         const uint32_t leader = elect_one_sync();
         bool ok = true;
         uint32_t s = 0, ph = 0;
-        for (int kb = kb0; kb < kb1; ++kb) {
+        for (int sb = sb0; sb < sb1; ++sb) {
             if (!mbar_wait_warp(full(s), ph)) { ok = false; break; }
             tc_fence_after();
             const uint64_t a = smem_desc_sw128(base + s * Cfg::SLOT, 16, 1024);
             const uint64_t b = smem_desc_sw128(base + s * Cfg::SLOT + Cfg::W_BYTES, 16, 1024);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)   // 32 bytes of k a step: +2 in the descriptors' 16-byte units
-                umma_i8_ss_if(tmem_base, a + 2 * j, b + 2 * j, Cfg::IDESC, (kb > kb0 || j > 0) ? 1u : 0u, leader);
+            for (int j = 0; j < 4 * KB; ++j)   // 32 bytes of k a step: +2 in the descriptors' 16-byte units
+                umma_i8_ss_if(tmem_base, a + (j / 4) * 1024 + 2 * (j % 4), b + (j / 4) * (BN * 8) + 2 * (j % 4), Cfg::IDESC,
+                              (sb > sb0 || j > 0) ? 1u : 0u, leader);
             umma_commit_if(empty(s), leader);
             if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
@@ -154,66 +173,79 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         if (!mbar_wait_warp(accf, 0) && lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
     } else {
         const int t = threadIdx.x - 64;
-        for (int j = t; j < cols; j += 128)
-            s_scale[j] = in_bounds(m0 + j, 1, p.M, kSiteI8GemmScale, status) ? p.q_scale[m0 + j] : 0.0f;
+        for (int j = t; j < BN; j += 256)
+            s_scale[j] = j < cols && in_bounds(m0 + j, 1, p.M, kSiteI8GemmScale, status) ? p.q_scale[m0 + j] : 0.0f;
         if (!mbar_wait_warp(accf, 0) && lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
     }
     tc_fence_before();
     __syncthreads();   // also publishes s_scale
     tc_fence_after();
 
-    const int quarter = warp & 3;            // TMEM lanes of this warp (warps 2..5)
+    const int quarter = warp & 3;            // TMEM lanes of this warp (warps 2..9)
+    const int eg = (warp - 2) >> 2;          // which of the quarter's two warps
     const int n_lane = quarter * 32 + lane;  // filter row inside the tile
     const int n = n0 + n_lane;
     const bool live = warp >= 2 && !*abort_flag;
     float ws = 0.0f, bias = 0.0f;
-    OUT *Y = static_cast<OUT *>(p.Y);
-    const long long y_elems = 1LL * p.M * p.N;
-    if (live && n < p.N && in_bounds(n, 1, p.N, kSiteI8GemmScale, status)) {
+    const bool has_n = n < p.N;
+    if (live && has_n && in_bounds(n, 1, p.N, kSiteI8GemmScale, status)) {
         ws = p.w_scale[n];
         if (p.bias) bias = p.bias[n];
     }
-    auto put = [&](int j, int acc) {   // column j of the tile
-        const long long at = 1LL * (m0 + j) * p.N + n;
-        const float v = static_cast<float>(acc) * s_scale[j] * ws;
-        if (n < p.N && in_bounds(at, 1, y_elems, kSiteI8GemmY, status)) i8_out(Y + at, p.bias ? v + bias : v);
+    const long long y_elems = 1LL * p.M * p.N;
+    const long long y0 = 1LL * m0 * p.N + n;
+    OUT *Y = static_cast<OUT *>(p.Y) + y0;
+    // columns j .. j + NB - 1 of the tile: a warp stores 32 neighbouring channels of a token
+    auto put = [&](int j, const int *acc, auto nb) {
+        constexpr int NB = decltype(nb)::value;
+        float v[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) v[i] = static_cast<float>(acc[i]) * s_scale[j + i] * ws;
+        if (p.bias) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) v[i] += bias;
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            if (has_n && j + i < cols && in_bounds(y0 + 1LL * (j + i) * p.N, 1, y_elems, kSiteI8GemmY, status))
+                i8_out(Y + 1LL * (j + i) * p.N, v[i]);
     };
     const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     if (S > 1) cluster_wait();
     if (live) {
 #pragma unroll 1
-        for (int j0 = 0; j0 < cols; j0 += 16) {
+        for (int j0 = eg * 16; j0 < cols; j0 += 32) {
             uint32_t r[16];
             tmem_ld_32x32b_x16(t_row + j0, r);
             tmem_wait_ld();
             if (S == 1) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (j0 + j < cols) put(j0 + j, static_cast<int>(r[j]));
+                put(j0, reinterpret_cast<const int *>(r), I8Int<16>());
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const int col = j0 + j;
-                    if (col >= cols) break;
-                    const uint32_t to = static_cast<uint32_t>(col / own);
-                    const uint32_t at = recv + ((rank * own + (col - to * own)) * 128 + n_lane) * 4;
-                    st_cluster_u32(map_rank(at, to), r[j]);
+                    const uint32_t col = static_cast<uint32_t>(j0 + j), to = col >> p.own_shift;
+                    const uint32_t at = recv + (((rank << p.own_shift) + (col - (to << p.own_shift))) * 128 + n_lane) * 4;
+                    if (j0 + j < cols) st_cluster_u32(map_rank(at, to), r[j]);
                 }
             }
         }
     }
     if (S > 1) {
         cluster_sync_all();
-        const int c0 = static_cast<int>(rank) * own;
+        const int c0 = static_cast<int>(rank << p.own_shift), own = 1 << p.own_shift;   // columns this CTA owns
         if (live) {
-            for (int j = 0; j < own && c0 + j < cols; ++j) {
-                int acc = 0;
+            for (int j = 2 * eg; j < own && c0 + j < cols; j += 4) {
+                int acc[2] = {0, 0};
                 for (uint32_t r = 0; r < S; ++r) {
-                    int v;
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(recv + ((r * own + j) * 128 + n_lane) * 4));
-                    acc += v;
+                    const uint32_t at = recv + (((r << p.own_shift) + j) * 128 + n_lane) * 4;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        int v;
+                        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at + i * 512));
+                        acc[i] += v;
+                    }
                 }
-                put(c0 + j, acc);
+                put(c0 + j, acc, I8Int<2>());
             }
         }
     }
@@ -226,56 +258,60 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 // ---------------------------------------------------------------------------------------
 // Many tokens: i8_pair_kernel
 // ---------------------------------------------------------------------------------------
-// A persistent CTA pair per 256 x 256 tile of Y (M = 256, N = 256 MMAs, cta_group::2): each CTA
-// stages 128 token rows and 128 filter rows per k block and receives its 128 tokens x 256 columns
-// of the accumulator. Two accumulators of 256 columns fill TMEM, so tile t + 1 multiplies while
-// tile t is scaled and stored.
-//   warp 0      TMA ring of STAGES slots (16 KB of tokens + 16 KB of filter per CTA)
+// A persistent CTA pair per 256 x BN tile of Y (M = 256, N = BN MMAs, cta_group::2): each CTA
+// stages 128 token rows and BN / 2 filter rows per k block and receives its 128 tokens x BN columns
+// of the accumulator. Two accumulators, so tile t + 1 multiplies while tile t is scaled and stored.
+//   warp 0      TMA ring of STAGES slots
 //   warp 1      TMEM allocation; the even CTA's issues the MMAs for both
 //   warps 2..9  epilogue, two warps per TMEM lane quarter taking alternate chunks of 128 bytes of
-//               output: tcgen05.ld, scale, round, swizzled staging, 16-byte stores
+//               output: tcgen05.ld, scale, round, swizzled staging, one tensor store a chunk. A
+//               warp fetches its columns' scales and biases into its own corner of shared memory
+//               before it waits for the accumulator, so their latency hides behind the MMAs.
+template <int BN_, int STAGES_>
 struct I8PairCfg {
-    static constexpr int BM = 128, BN = 256, STAGES = 6;   // per CTA: 128 rows; the pair: 256
-    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, SLOT = A_BYTES + B_BYTES;
+    static constexpr int BN = BN_, STAGES = STAGES_;   // per CTA: 128 rows; the pair: 256
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, SLOT = A_BYTES + B_BYTES;
     static constexpr int NUM_EPI = 8;
     static constexpr int EPI_BYTES = NUM_EPI * 32 * 128;
+    static constexpr int SCALE_BYTES = NUM_EPI * (BN / 2) * 8;   // a warp's columns: scale, bias
     static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
-    static constexpr int SMEM = 1024 + STAGES * SLOT + EPI_BYTES + NUM_BARS * 8 + 16;
+    static constexpr int SMEM = 1024 + STAGES * SLOT + EPI_BYTES + SCALE_BYTES + NUM_BARS * 8 + 16;
     static constexpr int THREADS = 32 * (2 + NUM_EPI);
     static constexpr uint32_t IDESC = idesc_i8_s32(256, BN);
-    static constexpr int GROUP = 8;   // row tiles walked together
+    static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
-static_assert(I8PairCfg::SMEM <= 232448, "shared memory of one CTA");
+
+constexpr int kI8Group = 8;   // row tiles walked together
 
 // Tile t of the walk: GROUP row tiles together, so that the CTAs in flight share their operands
 // in L2 (74 pairs in flight hold about 8 x 9 tiles).
 __device__ __forceinline__ void i8_tile(int t, int m_tiles, int n_tiles, int &mt, int &nt) {
-    const int per = I8PairCfg::GROUP * n_tiles;
+    const int per = kI8Group * n_tiles;
     const int g = t / per, r = t - g * per;
-    const int m_first = g * I8PairCfg::GROUP;
-    const int h = m_tiles - m_first < I8PairCfg::GROUP ? m_tiles - m_first : I8PairCfg::GROUP;
+    const int m_first = g * kI8Group;
+    const int h = m_tiles - m_first < kI8Group ? m_tiles - m_first : kI8Group;
     nt = r / h;
     mt = m_first + (r - nt * h);
 }
 
-template <typename OUT>
-__global__ void __launch_bounds__(I8PairCfg::THREADS, 1)
-i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmW, const I8GemmParams p,
-               unsigned int *status) {
-    using Cfg = I8PairCfg;
+template <class Cfg, typename OUT>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmW,
+               const __grid_constant__ CUtensorMap tmY, const I8GemmParams p, unsigned int *status) {
     grid_dependents_launch();
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw_base);
     constexpr uint32_t epi_off = Cfg::STAGES * Cfg::SLOT;
-    const uint32_t bars = base + epi_off + Cfg::EPI_BYTES;
+    constexpr uint32_t scale_off = epi_off + Cfg::EPI_BYTES;
+    const uint32_t bars = base + scale_off + Cfg::SCALE_BYTES;
     auto full = [&](int s) { return bars + 8u * s; };
     auto empty = [&](int s) { return bars + 8u * (Cfg::STAGES + s); };
     auto accf = [&](int b) { return bars + 8u * (2 * Cfg::STAGES + b); };
     auto acce = [&](int b) { return bars + 8u * (2 * Cfg::STAGES + 2 + b); };
     const uint32_t done_bar = bars + 8u * (2 * Cfg::STAGES + 4);
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + epi_off + Cfg::EPI_BYTES + Cfg::NUM_BARS * 8);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + scale_off + Cfg::SCALE_BYTES + Cfg::NUM_BARS * 8);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -296,9 +332,10 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmW);
+        if (p.vec) prefetch_tensormap(&tmY);
     }
     if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_holder), 512);
+        tmem_alloc_pair(smem_u32(tmem_holder), 2 * Cfg::BN);
         tmem_relinquish_pair();
     }
     tc_fence_before();
@@ -316,21 +353,19 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const int first = static_cast<int>(blockIdx.x >> 1), step = static_cast<int>(gridDim.x >> 1);
 
     if (warp == 0) {
+        const uint32_t leader = elect_one_sync();
         uint32_t it = 0, s = 0, ph = 0;
         bool ok = true;
         for (int t = first; t < p.num_tiles && ok && !*abort_flag; t += step) {
             int mt, nt;
             i8_tile(t, p.m_tiles, p.n_tiles, mt, nt);
-            const int row_q = mt * 256 + static_cast<int>(rank) * 128, row_w = nt * 256 + static_cast<int>(rank) * 128;
+            const int row_q = mt * 256 + static_cast<int>(rank) * 128, row_w = nt * Cfg::BN + static_cast<int>(rank) * (Cfg::BN / 2);
             for (int kb = 0; kb < p.num_kblk; ++kb, ++it) {
                 if (!mbar_wait_warp(empty(s), ph ^ 1u)) { ok = false; break; }
-                if (lane == 0) {
-                    const uint32_t slot = base + s * Cfg::SLOT;
-                    if (rank == 0) mbar_arrive_expect_tx(full(s), 2 * Cfg::SLOT);   // both CTAs' copies
-                    tma_load_2d_pair(slot, &tmQ, lead(full(s)), kb * 128, row_q);
-                    tma_load_2d_pair(slot + Cfg::A_BYTES, &tmW, lead(full(s)), kb * 128, row_w);
-                }
-                __syncwarp();
+                const uint32_t slot = base + s * Cfg::SLOT;
+                mbar_arrive_expect_tx_if(full(s), 2 * Cfg::SLOT, leader & (rank ^ 1u));   // both CTAs' copies
+                tma_load_2d_pair_if(slot, &tmQ, lead(full(s)), kb * 128, row_q, leader);
+                tma_load_2d_pair_if(slot + Cfg::A_BYTES, &tmW, lead(full(s)), kb * 128, row_w, leader);
                 if (++s == Cfg::STAGES) { s = 0; ph ^= 1u; }
             }
         }
@@ -372,9 +407,12 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
     } else {
         constexpr int CW = 128 / static_cast<int>(sizeof(OUT));   // columns of a 128-byte chunk
-        constexpr int V = 16 / static_cast<int>(sizeof(OUT));     // values of a 16-byte store
+        constexpr int V = 16 / static_cast<int>(sizeof(OUT));     // values of 16 bytes
+        constexpr int CHUNKS = Cfg::BN / CW / 2;                  // chunks a warp takes: eg, eg + 2, ...
         const int quarter = warp & 3, eg = (warp - 2) >> 2;
         const uint32_t stage = base + epi_off + (warp - 2) * 4096;
+        float *s_ws = reinterpret_cast<float *>(smem + scale_off) + (warp - 2) * Cfg::BN;   // CHUNKS x CW scales,
+        float *s_bias = s_ws + Cfg::BN / 2;                                                  // then biases
         OUT *Y = static_cast<OUT *>(p.Y);
         const long long y_elems = 1LL * p.M * p.N;
         uint32_t local = 0;
@@ -384,66 +422,71 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             int mt, nt;
             i8_tile(t, p.m_tiles, p.n_tiles, mt, nt);
             const int row0 = mt * 256 + static_cast<int>(rank) * 128 + quarter * 32;   // this warp's 32 rows
-            const int n0 = nt * 256;
-            const float qs = row0 + lane < p.M ? p.q_scale[row0 + lane] : 0.0f;
-            if (!mbar_wait_warp_backoff(accf(b), (local >> 1) & 1u, 64)) { if (lane == 0) fail(); break; }
+            const int n0 = nt * Cfg::BN;
+            const float qs = row0 + lane < p.M && in_bounds(row0 + lane, 1, p.M, kSiteI8GemmScale, status)
+                                 ? p.q_scale[row0 + lane] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < Cfg::BN / 64; ++i) {   // the warp's BN / 2 columns, 32 at a time
+                const int e = i * 32 + lane, c = n0 + (2 * (e / CW) + eg) * CW + e % CW;
+                const bool in = c < p.N && in_bounds(c, 1, p.N, kSiteI8GemmScale, status);
+                s_ws[e] = in ? p.w_scale[c] : 0.0f;
+                s_bias[e] = in && p.bias ? p.bias[c] : 0.0f;
+            }
+            __syncwarp();
+            if (!mbar_wait_backoff(accf(b), (local >> 1) & 1u, 32)) { if (lane == 0) fail(); break; }
             tc_fence_after();
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * Cfg::BN;
 #pragma unroll 1
-            for (int h = eg; h < Cfg::BN / CW; h += 2) {
-                const int c0 = n0 + h * CW;
-                if (c0 >= p.N) break;
-                // the scales and biases of the chunk's columns, CW / 32 a lane
-                float wsv[CW / 32], bv[CW / 32];
+            for (int k = 0; k < CHUNKS; ++k) {
+                const int h = 2 * k + eg, c0 = n0 + h * CW;
+                uint32_t r[CW / 16][16];
 #pragma unroll
-                for (int i = 0; i < CW / 32; ++i) {
-                    const int c = c0 + i * 32 + lane;
-                    wsv[i] = c < p.N ? p.w_scale[c] : 0.0f;
-                    bv[i] = c < p.N && p.bias ? p.bias[c] : 0.0f;
+                for (int g = 0; g < CW / 16; ++g) tmem_ld_32x32b_x16(t_row + h * CW + g * 16, r[g]);
+                tmem_wait_ld();
+                if (k == CHUNKS - 1) {   // the accumulator is read: the next tile but one may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(lead(acce(b)));
                 }
+                uint32_t packed[32];   // the lane's 128 bytes
 #pragma unroll
-                for (int g = 0; g < CW / 16; ++g) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(t_row + h * CW + g * 16, r);
-                    tmem_wait_ld();
-                    float v[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int from = (g * 16 + j) & 31;
-                        const float w = __shfl_sync(0xffffffffu, wsv[g / 2], from);
-                        v[j] = static_cast<float>(static_cast<int>(r[j])) * qs * w;
-                        if (p.bias) v[j] += __shfl_sync(0xffffffffu, bv[g / 2], from);
+                for (int g = 0; g < CW / 4; ++g) {
+                    const float4 w = *reinterpret_cast<const float4 *>(s_ws + k * CW + g * 4);
+                    const uint32_t *a = &r[g / 4][(g % 4) * 4];
+                    float v[4] = {static_cast<float>(static_cast<int>(a[0])) * qs * w.x,
+                                  static_cast<float>(static_cast<int>(a[1])) * qs * w.y,
+                                  static_cast<float>(static_cast<int>(a[2])) * qs * w.z,
+                                  static_cast<float>(static_cast<int>(a[3])) * qs * w.w};
+                    if (p.bias) {
+                        const float4 bb = *reinterpret_cast<const float4 *>(s_bias + k * CW + g * 4);
+                        v[0] += bb.x; v[1] += bb.y; v[2] += bb.z; v[3] += bb.w;
                     }
+                    if constexpr (sizeof(OUT) == 2) {
+                        packed[2 * g] = halo_pack_bf16x2(v[0], v[1]);
+                        packed[2 * g + 1] = halo_pack_bf16x2(v[2], v[3]);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 16 / V; ++i) {
-                        const uint32_t c = g * (16 / V) + i;   // 16-byte piece of the lane's 128-byte row
-                        const float *u = v + i * V;
-                        const uint32_t at = stage + lane * 128 + ((c ^ (lane & 7)) << 4);
-                        if constexpr (sizeof(OUT) == 2)
-                            st_shared_v4(at, halo_pack_bf16x2(u[0], u[1]), halo_pack_bf16x2(u[2], u[3]),
-                                         halo_pack_bf16x2(u[4], u[5]), halo_pack_bf16x2(u[6], u[7]));
-                        else
-                            st_shared_v4(at, __float_as_uint(u[0]), __float_as_uint(u[1]), __float_as_uint(u[2]),
-                                         __float_as_uint(u[3]));
+                        for (int i = 0; i < 4; ++i) packed[4 * g + i] = __float_as_uint(v[i]);
                     }
                 }
+                if (p.vec && lane == 0) bulk_wait_group_read0();   // the previous chunk has left the staging
                 __syncwarp();
-                if (p.vec) {   // 8 lanes a row, 4 rows an instruction
-                    const int col = c0 + (lane & 7) * V;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i * 4 + (lane >> 3), row = row0 + rr;
-                        const long long at = 1LL * row * p.N + col;
-                        if (row < p.M && col < p.N && in_bounds(at, V, y_elems, kSiteI8GemmY, status)) {
-                            uint32_t a, bb, c, d;
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(a), "=r"(bb), "=r"(c), "=r"(d)
-                                         : "r"(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4)));
-                            *reinterpret_cast<uint4 *>(Y + at) = make_uint4(a, bb, c, d);
-                        }
+                for (int c = 0; c < 8; ++c)   // 16-byte piece c of the lane's row, 128-byte swizzle
+                    st_shared_v4(stage + lane * 128 + ((c ^ (lane & 7)) << 4), packed[4 * c], packed[4 * c + 1],
+                                 packed[4 * c + 2], packed[4 * c + 3]);
+                if (p.vec) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0 && c0 < p.N && row0 < p.M) {   // rows and columns past Y are not stored
+                        tma_store_2d(&tmY, stage, c0, row0);
+                        bulk_commit_group();
                     }
-                } else {       // an element a lane, a row at a time
-                    for (int rr = 0; rr < 32 && row0 + rr < p.M; ++rr) {
+                } else {   // rows of Y off the 16-byte boundaries: an element a lane, a row at a time
+                    __syncwarp();
+                    const int rows = p.M - row0 < 32 ? p.M - row0 : 32;
+#pragma unroll 4
+                    for (int rr = 0; rr < rows; ++rr) {
 #pragma unroll
                         for (int i = 0; i < CW / 32; ++i) {
                             const int e = i * 32 + lane, col = c0 + e;
@@ -455,20 +498,16 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         }
                     }
                 }
-                __syncwarp();
             }
-            // the accumulator may be overwritten by the next tile but one
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(lead(acce(b)));
         }
+        if (lane == 0) bulk_wait_group0();   // the stores are complete before the CTA exits
     }
 
     tc_fence_before();
     __syncthreads();
     cluster_sync_all();   // neither CTA leaves while the other may still signal its barriers
     tc_fence_after();
-    if (warp == 1) tmem_dealloc_pair(tmem_base, 512);
+    if (warp == 1) tmem_dealloc_pair(tmem_base, 2 * Cfg::BN);
 }
 
 }  // namespace convb200

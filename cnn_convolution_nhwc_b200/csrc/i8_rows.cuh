@@ -47,32 +47,93 @@ __device__ __forceinline__ float i8_to_float(__nv_bfloat16 v) { return __bfloat1
 __device__ __forceinline__ float i8_round_to(float v, float) { return v; }
 __device__ __forceinline__ float i8_round_to(float v, __nv_bfloat16) { return __bfloat162float(__float2bfloat16_rn(v)); }
 
-// Eight consecutive values; `p` 16-byte aligned.
-__device__ __forceinline__ void i8_load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Pairs of float32 in one 64-bit register (sm_100's packed arithmetic: two values an instruction).
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_split(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+// The largest of three magnitudes; a NaN stays a NaN (its bits lie above infinity's).
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Eight consecutive values as they lie in memory (16-byte aligned), and as four pairs.
+template <typename T>
+struct I8Raw {
+    uint4 u[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ I8Raw<T> i8_raw_load(const T *p) {
+    I8Raw<T> r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.u[i] = reinterpret_cast<const uint4 *>(p)[i];
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ I8Raw<T> i8_raw_zero() {
+    I8Raw<T> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.u[i] = make_uint4(0, 0, 0, 0);
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void i8_raw_store(T *p, const I8Raw<T> &r) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4 *>(p)[i] = r.u[i];
+}
+__device__ __forceinline__ void i8_unpack(const I8Raw<__nv_bfloat16> &r, uint64_t (&t)[4]) {
+    const uint32_t w[4] = {r.u[0].x, r.u[0].y, r.u[0].z, r.u[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+__device__ __forceinline__ void i8_unpack(const I8Raw<float> &r, uint64_t (&t)[4]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        t[2 * i] = f2_pack(__uint_as_float(r.u[i].x), __uint_as_float(r.u[i].y));
+        t[2 * i + 1] = f2_pack(__uint_as_float(r.u[i].z), __uint_as_float(r.u[i].w));
     }
 }
-__device__ __forceinline__ void i8_load8(const float *p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-// Stores eight values that the type holds exactly.
-__device__ __forceinline__ void i8_store8(__nv_bfloat16 *p, const float (&v)[8]) {
+// Rounds four pairs to the type.
+__device__ __forceinline__ void i8_pack(const uint64_t (&t)[4], I8Raw<__nv_bfloat16> &r) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = __byte_perm(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), 0x7632);
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_split(t[i], lo, hi);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        w[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    r.u[0] = make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ void i8_store8(float *p, const float (&v)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void i8_pack(const uint64_t (&t)[4], I8Raw<float> &r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float a, b, c, d;
+        f2_split(t[2 * i], a, b);
+        f2_split(t[2 * i + 1], c, d);
+        r.u[i] = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
+    }
 }
 
 // silu(a) * b in float32, silu(a) = a / (1 + exp(-a)). With e = exp(-|a|) <= 1 the quotient is
@@ -100,9 +161,12 @@ __device__ __forceinline__ I8RowScale i8_row_scale(uint32_t amax_bits, bool fini
     return s;
 }
 
-// The nearest integer of 127 t / A where the float32 product r = t * inv lies near a half.
-__device__ __noinline__ float i8_round_near_half(float t, float A, float r) {
-    const float lo = floorf(r);
+constexpr float kI8Magic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
+constexpr float kI8NearHalf = 0.49996f;
+
+// The nearest integer of 127 t / A where t * inv lies near a half.
+__device__ __noinline__ float i8_round_near_half(float t, float A, float inv) {
+    const float lo = floorf(t * inv);
     const double have = static_cast<double>(t) * 127.0, half = (static_cast<double>(lo) + 0.5) * static_cast<double>(A);
     if (have > half) return lo + 1.0f;
     if (have < half) return lo;
@@ -111,34 +175,53 @@ __device__ __noinline__ float i8_round_near_half(float t, float A, float r) {
 
 // Rounds one value (the low byte of the result).
 __device__ __forceinline__ uint32_t i8_quant1(float t, const I8RowScale &s) {
-    constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
     const float v = s.dead ? 0.0f : t * s.up;
-    const float r = v * s.inv;
-    float m = r + kMagic;
-    if (fabsf(r - (m - kMagic)) > 0.49996f) m = i8_round_near_half(v, s.A, r) + kMagic;
+    float m = fmaf(v, s.inv, kI8Magic);
+    if (fabsf(fmaf(v, s.inv, kI8Magic - m)) > kI8NearHalf) m = i8_round_near_half(v, s.A, s.inv) + kI8Magic;
     return __float_as_uint(m);
 }
 
-// Rounds eight values of a row to eight bytes (byte i of the pair of words is value i).
-__device__ __forceinline__ uint2 i8_quant8(const float (&t)[8], const I8RowScale &s) {
-    constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
-    uint32_t b[8];
+// Rounds eight values of a live row, already times `up`, to eight bytes (byte i of the pair of
+// words is value i).
+__device__ __forceinline__ uint2 i8_quant8(const uint64_t (&t)[4], const I8RowScale &s) {
+    const uint64_t inv = f2_pack(s.inv, s.inv), magic = f2_pack(kI8Magic, kI8Magic), minus1 = f2_pack(-1.0f, -1.0f);
+    uint64_t m[4];
     float worst = 0.0f;
-    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = s.dead ? 0.0f : t[i] * s.up;
-        const float r = v[i] * s.inv;
-        const float m = r + kMagic;
-        b[i] = __float_as_uint(m);
-        worst = fmaxf(worst, fabsf(r - (m - kMagic)));
+    for (int i = 0; i < 4; ++i) {
+        m[i] = f2_fma(t[i], inv, magic);
+        const uint64_t off = f2_fma(t[i], inv, f2_fma(m[i], minus1, magic));   // t * inv less the integer
+        float lo, hi;
+        f2_split(off, lo, hi);
+        worst = max3_abs(worst, lo, hi);
     }
-    if (worst > 0.49996f) {
+    uint32_t b[8];
 #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        f2_split(m[i], lo, hi);
+        b[2 * i] = __float_as_uint(lo);
+        b[2 * i + 1] = __float_as_uint(hi);
+    }
+    if (worst > kI8NearHalf) {
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-            const float r = v[i] * s.inv;
-            if (fabsf(r - (__uint_as_float(b[i]) - kMagic)) > 0.49996f)
-                b[i] = __float_as_uint(i8_round_near_half(v[i], s.A, r) + kMagic);
+            // selected by constant indices, so that the arrays stay in registers
+            float v = 0.0f;
+            uint32_t have = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                f2_split(t[j], lo, hi);
+                if (i == 2 * j) { v = lo; have = b[2 * j]; }
+                if (i == 2 * j + 1) { v = hi; have = b[2 * j + 1]; }
+            }
+            if (fabsf(fmaf(v, s.inv, kI8Magic - __uint_as_float(have))) > kI8NearHalf) {
+                have = __float_as_uint(i8_round_near_half(v, s.A, s.inv) + kI8Magic);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (i == j) b[j] = have;
+            }
         }
     }
     const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
@@ -146,131 +229,162 @@ __device__ __forceinline__ uint2 i8_quant8(const float (&t)[8], const I8RowScale
     return make_uint2(lo, hi);
 }
 
-// One row per group of `tpr` threads: a warp (GROUP_WARP, rows up to 256 * NV values) or a block.
-// A thread holds NV groups of eight values in registers, so a row of up to tpr * 8 * NV values
-// is read once; a longer row (STREAM) is walked in pieces of that size twice, the second time
-// from h (or x), which the first pass left in L2.
-// VEC: rows start on 16-byte boundaries and C is a multiple of 8; a thread's eight values are
-// neighbours. Otherwise they are tpr apart, one element per access.
-template <typename T, int MODE, int NV, bool VEC, bool GROUP_WARP, bool STREAM>
-__global__ void __launch_bounds__(GROUP_WARP ? 256 : 512)
+// One row per group of threads: a warp (TPR = 32) or a block. A thread holds NV groups of eight
+// values in registers, so a row of up to 8 * NV values a thread is read once; a longer row (STREAM)
+// is walked in pieces of that size twice, the second time from h (or x), which the first pass
+// left in L2. All of a thread's loads are issued before the first is used: with four groups a
+// thread that keeps 100 KB and more of loads in flight per SM.
+// VEC: tensors on 16 bytes and C a multiple of 8; a thread's eight values are neighbours and move in
+// 16-byte accesses; a block has the threads that the row needs (TPR = 0). Otherwise any C and any
+// pointers: neighbouring lanes hold neighbouring values, an element an access, and a thread's values
+// are TPR apart, a constant, so that its accesses need no address arithmetic.
+template <typename T, int MODE, int NV, bool VEC, int TPR, bool STREAM>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : 512)
 i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
     grid_dependents_launch();   // programmatic dependent launch (see ptx.cuh)
     grid_dependency_wait();
     constexpr bool NORM = MODE == kI8Norm || MODE == kI8NormResidual;
-    __shared__ float s_sum[32];
-    __shared__ uint32_t s_max[32];
+    constexpr bool GROUP_WARP = TPR == 32;
+    __shared__ float s_sum[16];
+    __shared__ uint32_t s_max[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tpr = GROUP_WARP ? 32 : static_cast<int>(blockDim.x);
+    const int tpr = TPR != 0 ? TPR : static_cast<int>(blockDim.x);
     const int tid = GROUP_WARP ? lane : static_cast<int>(threadIdx.x);
     const long long row = GROUP_WARP ? 1LL * blockIdx.x * (blockDim.x >> 5) + warp : static_cast<long long>(blockIdx.x);
     if (row >= p.M) return;   // whole warps only, and no block barrier follows for GROUP_WARP
     const int C = p.C;
-    const long long x_elems = p.M * C * (MODE == kI8Glu ? 2 : 1), n_elems = p.M * C;   // bounds checks (debug build)
-    const T *x = static_cast<const T *>(p.x);
-    const T *res = static_cast<const T *>(p.residual);
-    T *h = static_cast<T *>(p.h);
     const long long xrow = row * C * (MODE == kI8Glu ? 2 : 1), hrow = row * C;
+    const long long n_elems = p.M * C, x_elems = n_elems * (MODE == kI8Glu ? 2 : 1);   // bounds checks (debug build)
+    const T *x = static_cast<const T *>(p.x) + xrow;
+    const T *second = MODE == kI8Glu ? x + C : static_cast<const T *>(p.residual) + hrow;   // up, or the residual
+    T *h = static_cast<T *>(p.h) + hrow;
+    int8_t *q = p.q + row * p.ldq;
 
-    // element index of value i of group k in the piece that starts at c0
+    // column of value i of group k in the piece that starts at c0
     auto at = [&](int c0, int k, int i) { return VEC ? c0 + (k * tpr + tid) * 8 + i : c0 + (k * 8 + i) * tpr + tid; };
 
-    // Reads group k: the values t that are rounded, and (norms) adds the squares of h to `sum`.
+    // Reads a piece: the values t that are rounded; the norms add the squares of h to `sum`.
     // first: the row's first pass, which writes h.
-    auto load = [&](int c0, int k, bool first, float (&t)[8], float &sum) {
+    auto load = [&](int c0, bool first, uint64_t (&t)[NV][4], uint64_t &sum) {
+        const bool from_h = MODE == kI8NormResidual && !first;
+        const bool two = MODE == kI8Glu || (MODE == kI8NormResidual && first);
+        const T *src = from_h ? h : x;
         if constexpr (VEC) {
-            const int c = at(c0, k, 0);
-            if (c >= C) {
+            I8Raw<T> a[NV], b[NV];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t[i] = 0.0f;
-                return;
+            for (int k = 0; k < NV; ++k) {
+                const int c = at(c0, k, 0);
+                const bool in = c < C && in_bounds(xrow + c, 8, x_elems, kSiteI8RowsX, status);
+                a[k] = in ? i8_raw_load(src + c) : i8_raw_zero<T>();
+                if (two) b[k] = in ? i8_raw_load(second + c) : i8_raw_zero<T>();
             }
-            const bool from_h = MODE == kI8NormResidual && !first;
-            if (!in_bounds(from_h ? hrow + c : xrow + c, 8, x_elems, kSiteI8RowsX, status)) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t[i] = 0.0f;
-                return;
-            }
-            i8_load8(from_h ? h + hrow + c : x + xrow + c, t);
-            if constexpr (MODE == kI8Glu) {
-                float up[8];
-                i8_load8(x + xrow + C + c, up);
+            for (int k = 0; k < NV; ++k) {
+                const int c = at(c0, k, 0);
+                i8_unpack(a[k], t[k]);
+                uint64_t u[4];
+                if constexpr (MODE == kI8Glu) {
+                    i8_unpack(b[k], u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t[i] = i8_glu(t[i], up[i]);
-            }
-            if constexpr (MODE == kI8NormResidual) {
-                if (first) {
-                    float r[8];
-                    i8_load8(res + hrow + c, r);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) t[i] = i8_round_to(t[i] + r[i], T());
-                    i8_store8(h + hrow + c, t);
+                    for (int i = 0; i < 4; ++i) {
+                        float g0, g1, u0, u1;
+                        f2_split(t[k][i], g0, g1);
+                        f2_split(u[i], u0, u1);
+                        t[k][i] = f2_pack(i8_glu(g0, u0), i8_glu(g1, u1));
+                    }
                 }
-            }
-            if constexpr (NORM) {
-                float w[8];
-                i8_load8(p.weight + c, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    sum = fmaf(t[i], t[i], sum);
-                    t[i] *= w[i];
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = at(c0, k, i);
-                t[i] = 0.0f;
-                if (c >= C || !in_bounds(xrow + c, 1, x_elems, kSiteI8RowsX, status)) continue;
-                float v;
-                if (MODE == kI8NormResidual && !first) v = i8_to_float(h[hrow + c]);
-                else v = i8_to_float(x[xrow + c]);
-                if constexpr (MODE == kI8Glu) v = i8_glu(v, i8_to_float(x[xrow + C + c]));
                 if constexpr (MODE == kI8NormResidual) {
                     if (first) {
-                        v = i8_round_to(v + i8_to_float(res[hrow + c]), T());
-                        h[hrow + c] = static_cast<T>(v);
+                        i8_unpack(b[k], u);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) t[k][i] = f2_add(t[k][i], u[i]);
+                        i8_pack(t[k], a[k]);
+                        i8_unpack(a[k], t[k]);
+                        if (c < C) i8_raw_store(h + c, a[k]);
                     }
                 }
                 if constexpr (NORM) {
-                    sum = fmaf(v, v, sum);
-                    v *= p.weight[c];
+                    uint64_t w[4];
+                    i8_unpack(i8_raw_load(p.weight + (c < C ? c : 0)), w);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        sum = f2_fma(t[k][i], t[k][i], sum);
+                        t[k][i] = f2_mul(t[k][i], w[i]);
+                    }
                 }
-                t[i] = v;
+            }
+        } else {
+            float a[NV][8], b[NV][8], w[NV][8];
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = at(c0, k, i);
+                    const bool in = c < C && in_bounds(xrow + c, 1, x_elems, kSiteI8RowsX, status);
+                    a[k][i] = in ? i8_to_float(src[c]) : 0.0f;
+                    if (two) b[k][i] = in ? i8_to_float(second[c]) : 0.0f;
+                    if (NORM) w[k][i] = c < C ? p.weight[c] : 0.0f;
+                }
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int c = at(c0, k, i);
+                    if constexpr (MODE == kI8Glu) a[k][i] = i8_glu(a[k][i], b[k][i]);
+                    if constexpr (MODE == kI8NormResidual) {
+                        if (first) {
+                            a[k][i] = i8_round_to(a[k][i] + b[k][i], T());
+                            if (c < C) h[c] = static_cast<T>(a[k][i]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    t[k][i] = f2_pack(a[k][2 * i], a[k][2 * i + 1]);
+                    if constexpr (NORM) {
+                        sum = f2_fma(t[k][i], t[k][i], sum);
+                        t[k][i] = f2_mul(t[k][i], f2_pack(w[k][2 * i], w[k][2 * i + 1]));
+                    }
+                }
             }
         }
     };
-    auto store = [&](int c0, int k, const float (&t)[8], const I8RowScale &s) {
-        const uint2 b = i8_quant8(t, s);
-        int8_t *qrow = p.q + row * p.ldq;
+    auto store = [&](int c0, int k, uint2 b) {
         if constexpr (VEC) {
             const int c = at(c0, k, 0);
-            if (c < C && in_bounds(hrow + c, 8, n_elems, kSiteI8RowsQ, status)) *reinterpret_cast<uint2 *>(qrow + c) = b;
+            if (c < C && in_bounds(hrow + c, 8, n_elems, kSiteI8RowsQ, status)) *reinterpret_cast<uint2 *>(q + c) = b;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = at(c0, k, i);
                 if (c < C && in_bounds(hrow + c, 1, n_elems, kSiteI8RowsQ, status))
-                    qrow[c] = static_cast<int8_t>((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
+                    q[c] = static_cast<int8_t>((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
             }
         }
     };
 
-    float t[NV][8];
-    float sum = 0.0f;
-    uint32_t amax = 0u;   // of the magnitudes' bits: ordered like them, with infinity and NaN above
+    uint64_t t[NV][4];
+    uint64_t sum2 = 0;      // of the squares, even and odd values apart
+    float top = 0.0f;       // the largest magnitude, or NaN
     const int piece = tpr * 8 * NV;
     for (int c0 = 0; c0 < (STREAM ? C : 1); c0 += piece) {
-#pragma unroll
-        for (int k = 0; k < NV; ++k) load(c0, k, true, t[k], sum);
+        load(c0, true, t, sum2);
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(t[k][i]) & 0x7fffffffu);
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi;
+                f2_split(t[k][i], lo, hi);
+                top = max3_abs(top, lo, hi);
+            }
         if (C - c0 <= piece) break;   // c0 + piece may pass the int range
     }
-    amax = __reduce_max_sync(0xffffffffu, amax);
+    uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);   // magnitudes are ordered as their bits
+    float sum = 0.0f;
     if constexpr (NORM) {
+        float lo, hi;
+        f2_split(sum2, lo, hi);
+        sum = lo + hi;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
@@ -285,7 +399,8 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
         if constexpr (NORM) {
             sum = lane < warps ? s_sum[lane] : 0.0f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            sum = __shfl_sync(0xffffffffu, sum, 0);
         }
     }
     const bool finite = amax < 0x7f800000u && (!NORM || sum < __uint_as_float(0x7f800000u));
@@ -298,13 +413,17 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
         if (in_bounds(row, 1, p.M, kSiteI8RowsScale, status)) p.scale[row] = sc;
     }
     for (int c0 = 0; c0 < (STREAM ? C : 1); c0 += piece) {
+        if constexpr (STREAM) {
+            uint64_t unused = 0;
+            load(c0, false, t, unused);
+        }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if constexpr (STREAM) {
-                float unused = 0.0f;
-                load(c0, k, false, t[k], unused);
+            if (s.up != 1.0f) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[k][i] = f2_mul(t[k][i], f2_pack(s.up, s.up));
             }
-            store(c0, k, t[k], s);
+            store(c0, k, s.dead ? make_uint2(0u, 0u) : i8_quant8(t[k], s));
         }
         if (C - c0 <= piece) break;
     }

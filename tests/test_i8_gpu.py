@@ -167,8 +167,8 @@ def test_dequant(cb, M, C, dtype):
     assert torch.equal(y, (q.float() * scale[:, None]).to(dtype))
 
 
-VARIANTS = ["", "pair", "split,16,1", "split,32,2", "split,64,4", "split,128,8", "split,128,1", "split,16,8"]
-SHAPES = [(1, 1, 1), (1, 16, 8), (2, 17, 7), (5, 127, 129), (16, 128, 128), (17, 129, 300), (33, 1000, 257), (64, 1024, 512),
+VARIANTS = ["", "pair,256", "pair,128", "split,16,1", "split,32,2", "split,64,4", "split,128,8", "split,128,1", "split,16,8"]
+SHAPES = [(1, 1, 1), (1, 16, 8), (2, 17, 7), (3, 256, 128), (40, 384, 250), (90, 640, 140), (31, 1152, 300), (5, 127, 129), (16, 128, 128), (17, 129, 300), (33, 1000, 257), (64, 1024, 512),
           (65, 1030, 1000), (128, 500, 1001), (129, 4096, 136), (300, 1100, 264), (513, 272, 520), (1000, 96, 777)]
 
 
@@ -338,6 +338,36 @@ def test_gap_between_rows_is_left_alone(cb):
         assert torch.all(base[:M, C:] == 55) and torch.all(base[M] == 55)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("M,C", [(3, 40), (5, 1001), (2, 5000)])
+def test_tensors_off_16_bytes(cb, M, C, dtype):
+    g = _gen(M, C, 5)
+
+    def view(n):   # starts one element into its storage
+        return _normal(g, n + 1, dtype=dtype)[1:]
+    x, r = view(M * C).view(M, C), view(M * C).view(M, C)
+    w = 1 + 0.1 * _normal(g, C + 1)[1:]
+    h = view(M * C).view(M, C)
+    q, scale, h = cb.rmsnorm_i8_fwd(x, w, r, h=h)
+    rq, rs, rh = ref.rmsnorm(x, w, r)
+    assert torch.equal(h.cpu(), rh) and np.array_equal(_q(q), rq)
+    x2 = view(M * 2 * C).view(M, 2 * C)
+    for a, b in ((cb.quant_rows_i8_fwd(x), cb.quant_rows_i8_fwd(x.clone())),
+                 (cb.quant_rows_i8_fwd(x2, glu=True), cb.quant_rows_i8_fwd(x2.clone(), glu=True)),
+                 (cb.quant_filter_i8_fwd(x), cb.quant_filter_i8_fwd(x.clone()))):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    y = view(M * C).view(M, C)
+    assert torch.equal(cb.dequant_rows_i8_fwd(q, scale, y=y), cb.dequant_rows_i8_fwd(q, scale, dtype=dtype))
+    wq, ws = cb.quant_filter_i8_fwd(_normal(g, C, 64))
+    y = view(M * 64).view(M, 64)
+    for v in ("", "pair,256", "pair,128"):
+        os.environ["CONV_B200_I8"] = v
+        try:
+            assert torch.equal(cb.pointwise_i8_fwd(q, scale, wq, ws, y=y), cb.pointwise_i8_fwd(q, scale, wq, ws, dtype=dtype))
+        finally:
+            del os.environ["CONV_B200_I8"]
+
+
 CHILD = r'''
 import os, sys
 import numpy as np
@@ -362,7 +392,7 @@ def run_all(cb):
             q2, s2 = cb.quant_rows_i8_fwd(torch.cat([x, r], dim=1), glu=True)
             w, ws = cb.quant_filter_i8_fwd(_normal(g, C, N, dtype=dtype))
             ys = []
-            for v in ("", "pair", "split,16,1", "split,64,1"):
+            for v in ("", "pair,256", "pair,128", "split,16,1", "split,64,1"):
                 os.environ["CONV_B200_I8"] = v
                 ys.append(cb.pointwise_i8_fwd(q, s, w, ws, _normal(g, N), dtype=dtype))
             os.environ.pop("CONV_B200_I8")
