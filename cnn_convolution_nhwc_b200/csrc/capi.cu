@@ -97,7 +97,7 @@ struct DeviceState {
     bool ready = false;
     int num_sms = 0;
     unsigned int *status = nullptr;   // device address of g_conv_status on this device
-    std::atomic<unsigned long long> attr_done[2] = {{0}, {0}};   // bit per kernel whose shared-memory limit is raised
+    std::atomic<unsigned long long> attr_done[3] = {{0}, {0}, {0}};   // bit per kernel whose shared-memory limit is raised
     cublasHandle_t blas = nullptr;    // for the explicit-im2col comparison path, made on first use
     void *im2col_scratch = nullptr;   // device address of g_im2col_scratch on this device
     // clusters of a kernel that fit on the device at once, per (kernel bit, cluster size, shared

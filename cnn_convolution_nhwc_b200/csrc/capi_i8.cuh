@@ -51,6 +51,44 @@ int run_i8_rows(const I8RowsParams &p, int dtype, cudaStream_t stream, DeviceSta
     return dtype == CONV_F32 ? run_i8_rows<float, MODE>(p, stream, d) : run_i8_rows<__nv_bfloat16, MODE>(p, stream, d);
 }
 
+// ---- filter ------------------------------------------------------------------------------
+template <typename T, bool VEC>
+int launch_i8_filter(const I8FilterParams &p, int S, cudaStream_t stream, DeviceState *d, unsigned bit) {
+    auto kern = i8_filter_kernel<T, VEC>;
+    if (int rc = ensure_smem_attr(d, bit, kern, 200 * 1024)) return rc;
+    const long long ctas = 1LL * ((p.Cout + kI8FilterCols - 1) / kI8FilterCols) * S;
+    if (ctas > kInt32Max) return CONV_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = static_cast<size_t>(i8_filter_smem(p.piece, sizeof(T)));
+    cfg.stream = stream;
+    return launched(launch_k(cfg, kern, p, d->status), "i8_filter_kernel");
+}
+
+template <typename T>
+int run_i8_filter(I8FilterParams p, cudaStream_t stream, DeviceState *d) {
+    // 128 rows a CTA until the cluster has eight, then more. A share up to a whole SM's shared memory
+    // is read once; a longer one in pieces of a quarter of it, twice.
+    const int tiles = (p.Cin + 127) / 128;
+    int S = 1;
+    while (S < 8 && S < tiles) S *= 2;
+    p.share = (tiles + S - 1) / S * 128;
+    constexpr int tile_bytes = i8_filter_smem(128, sizeof(T));
+    const int quarter = 54 * 1024 / tile_bytes * 128, all = 200 * 1024 / tile_bytes * 128;
+    p.piece = p.share <= all ? p.share : quarter;
+    const bool vec = p.Cout % 8 == 0 && aligned(p.F, 16);
+    constexpr unsigned bit = sizeof(T) == 4 ? 130 : 128;
+    return vec ? launch_i8_filter<T, true>(p, S, stream, d, bit) : launch_i8_filter<T, false>(p, S, stream, d, bit + 1);
+}
+
 // ---- product -----------------------------------------------------------------------------
 // A matrix of 8-bit rows in boxes of 128 values x `box_rows` rows, 128-byte swizzle; with kb > 1 the
 // values are split into blocks of 128 (C a multiple of 128) and a box has kb of them.
@@ -181,7 +219,7 @@ int run_i8_product(const I8Operands &a, I8GemmParams p, cudaStream_t stream, Dev
     p.num_kblk = (a.Cin + 127) / 128;
     p.vec = aligned(p.Y, 16) && (1LL * p.N * sizeof(OUT)) % 16 == 0;
     const I8Plan pl = plan_i8(p.M, p.N, p.num_kblk, d->num_sms);
-    constexpr unsigned bit = sizeof(OUT) == 4 ? 120 : 112;
+    constexpr unsigned bit = sizeof(OUT) == 4 ? 148 : 132;
     if (pl.pair)
         return pl.bn == 256 ? launch_i8_pair<I8PairCfg<256, 5>, OUT>(a, p, stream, d, bit)
                             : launch_i8_pair<I8PairCfg<128, 7>, OUT>(a, p, stream, d, bit + 1);
@@ -298,33 +336,7 @@ int quant_filter_i8_fwd(const void *F, int8_t *Wq, float *scale, int Cin, int Co
     p.Cin = Cin;
     p.Cout = Cout;
     p.ldq = ldw;
-    // a tile of rows per CTA until the cluster has eight, then more tiles each
-    const int tiles = (Cin + kI8FilterRows - 1) / kI8FilterRows;
-    int S = 1;
-    while (S < 8 && S < tiles) S *= 2;
-    p.slab = (tiles + S - 1) / S * kI8FilterRows;
-    const long long ctas = 1LL * ((Cout + kI8FilterCols - 1) / kI8FilterCols) * S;
-    if (ctas > kInt32Max) return CONV_ERR_UNSUPPORTED;
-    const bool vec = Cout % 8 == 0 && aligned(F, 16);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaError_t rc;
-    if (dtype == CONV_F32)
-        rc = vec ? launch_k(cfg, i8_filter_kernel<float, true>, p, d->status)
-                 : launch_k(cfg, i8_filter_kernel<float, false>, p, d->status);
-    else
-        rc = vec ? launch_k(cfg, i8_filter_kernel<__nv_bfloat16, true>, p, d->status)
-                 : launch_k(cfg, i8_filter_kernel<__nv_bfloat16, false>, p, d->status);
-    return launched(rc, "i8_filter_kernel");
+    return dtype == CONV_F32 ? run_i8_filter<float>(p, stream, d) : run_i8_filter<__nv_bfloat16>(p, stream, d);
 }
 
 int dequant_rows_i8_fwd(const int8_t *q, const float *scale, void *y, int M, int C, int ldq, int dtype,

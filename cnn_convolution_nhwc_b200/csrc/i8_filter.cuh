@@ -4,9 +4,14 @@
 // q = 127 F[c][o] / A[o] rounded to nearest even (the rules of i8_rows.cuh), scale[o] = A[o] / 127.
 // The result is stored transposed, Wq [Cout][Cin], so that both operands of the 8-bit product run
 // along the reduction. A column's maximum needs all of Cin before its first byte can be written:
-// a cluster of S CTAs holds the column block, each CTA a slab of rows; the CTAs' maxima meet in
-// distributed shared memory, and the second pass reads the slab again from L2 (the blocks in
-// flight hold 148 slabs of a few tens of KB, well inside the 126 MB), so DRAM is read once.
+// a cluster of S CTAs holds 32 columns, each CTA a share of the rows in shared memory (staged by
+// asynchronous copies, all in flight at once), and the CTAs' maxima meet in distributed shared
+// memory. The filter is read once; a share beyond shared memory is walked in pieces twice, the
+// second time mostly from L2. Rounded bytes are transposed through a second tile, four rows of a
+// column to a word, whose 16-byte chunks are permuted by the column so that neither the words'
+// stores nor the chunks' loads meet in a bank, and leave as 16-byte stores. 32 columns (64 bytes of a
+// bf16 row) rather than 64 keep a CTA small enough for four on an SM, whose loads, maxima and
+// stores overlap: 4096 x 16384 in bf16 took 90 us with 64.
 #pragma once
 #include "i8_rows.cuh"
 
@@ -17,66 +22,115 @@ struct I8FilterParams {
     int8_t *q;         // [Cout] rows of Cin bytes, ldq apart
     float *scale;      // [Cout]
     int Cin, Cout, ldq;
-    int slab;          // rows per CTA, a multiple of kI8FilterRows
+    int share;         // rows per CTA, a multiple of 128
+    int piece;         // rows in shared memory at once, a multiple of 128
 };
 
-constexpr int kI8FilterCols = 64;    // columns per cluster: 128 bytes of a bf16 row
-constexpr int kI8FilterRows = 128;   // rows per transposed tile: a warp's 4 rows x 8 warps x 4 row groups
-constexpr int kI8FilterPitch = kI8FilterRows + 4;   // bytes between a tile's columns: 33 words
+constexpr int kI8FilterCols = 32;
 
-// VEC: Cout a multiple of 8 and F 16-byte aligned.
+__host__ __device__ constexpr int i8_filter_smem(int piece, int elem) { return piece * kI8FilterCols * (elem + 1); }
+
+// VEC: rows of F on 16-byte boundaries (Cout a multiple of 8).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
     grid_dependents_launch();
     grid_dependency_wait();
+    extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ uint32_t s_part[8][kI8FilterCols];
     __shared__ uint32_t s_max[kI8FilterCols];        // this CTA's maxima, read by the cluster
-    __shared__ __align__(16) uint8_t s_tile[kI8FilterCols * kI8FilterPitch];
+    constexpr int ROW = kI8FilterCols * sizeof(T);   // bytes of a staged row
+    constexpr int CHUNKS = ROW / 16;
+    T *slab = reinterpret_cast<T *>(dyn);                    // [piece][32]
+    uint8_t *tile = dyn + static_cast<size_t>(p.piece) * ROW;  // [32][piece] bytes
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t S, rank;
+    uint32_t S;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
-    rank = cluster_rank();
+    const uint32_t rank = cluster_rank();
     const int o0 = static_cast<int>(blockIdx.x / S) * kI8FilterCols;
-    const int c0 = static_cast<int>(rank) * p.slab;
-    const int c1 = p.Cin - c0 < p.slab ? p.Cin : c0 + p.slab;   // c0 may pass Cin: an empty slab
-    const int cg = (lane & 7) * 8;                   // this thread's eight columns in the block
+    const int c0 = static_cast<int>(rank) * p.share;
+    const int c1 = p.Cin - c0 < p.share ? p.Cin : c0 + p.share;   // c0 may pass Cin: an empty share
+    const int cg = (lane & 7) * 4;                                // this thread's four columns in the block
+    const int rg = warp * 4 + (lane >> 3);                        // its row, or group of four rows, modulo 32
     const long long f_elems = 1LL * p.Cin * p.Cout, q_elems = f_elems;
     const T *F = static_cast<const T *>(p.F);
+    const bool once = c1 - c0 <= p.piece;   // the share stays in shared memory between the passes
 
-    auto load = [&](int c, float (&v)[8]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        if (c >= c1) return;
-        const long long at = 1LL * c * p.Cout + o0 + cg;
+    // Rows b0 .. b1 - 1 into the slab, zeros in the columns past Cout and up to a multiple of four rows.
+    auto stage = [&](int b0, int b1) {
+        const int rows = (b1 - b0 + 3) & ~3;
         if constexpr (VEC) {
-            if (o0 + cg < p.Cout && in_bounds(at, 8, f_elems, kSiteI8FilterF, status)) {
-                uint64_t t[4];
-                i8_unpack(i8_raw_load(F + at), t);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f2_split(t[i], v[2 * i], v[2 * i + 1]);
+            for (int i = threadIdx.x; i < rows * CHUNKS; i += 256) {
+                const int r = i / CHUNKS, e = (i % CHUNKS) * (16 / static_cast<int>(sizeof(T)));
+                const long long at = 1LL * (b0 + r) * p.Cout + o0 + e;
+                const bool in = b0 + r < b1 && o0 + e < p.Cout &&
+                                in_bounds(at, 16 / sizeof(T), f_elems, kSiteI8FilterF, status);
+                const uint32_t dst = smem_u32(slab) + r * ROW + e * static_cast<int>(sizeof(T));
+                if (in) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(F + at) : "memory");
+                else asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
             }
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
         } else {
+            // a column a lane, eight rows at a time
+            const int e = lane;
+            for (int r0 = warp; r0 < rows; r0 += 64) {
+                T v[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (o0 + cg + i < p.Cout && in_bounds(at + i, 1, f_elems, kSiteI8FilterF, status))
-                    v[i] = i8_to_float(F[at + i]);
+                for (int j = 0; j < 8; ++j) {
+                    const int r = r0 + 8 * j;
+                    const long long at = 1LL * (b0 + r) * p.Cout + o0 + e;
+                    v[j] = static_cast<T>(0.0f);
+                    if (b0 + r < b1 && o0 + e < p.Cout && in_bounds(at, 1, f_elems, kSiteI8FilterF, status)) v[j] = F[at];
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (r0 + 8 * j < rows) slab[(r0 + 8 * j) * kI8FilterCols + e] = v[j];
+            }
+        }
+        __syncthreads();
+    };
+
+    // four neighbouring values of a staged row
+    auto four = [&](int r, uint64_t &a, uint64_t &b) {
+        if constexpr (sizeof(T) == 2) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(slab + r * kI8FilterCols + cg);
+            a = f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+            b = f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+        } else {
+            const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(slab + r * kI8FilterCols + cg);
+            a = u.x;
+            b = u.y;
         }
     };
 
-    uint32_t amax[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-    for (int c = c0 + warp * 4 + (lane >> 3); c < c1; c += 32) {
-        float v[8];
-        load(c, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax[i] = max(amax[i], __float_as_uint(v[i]) & 0x7fffffffu);
+    float top[4] = {0, 0, 0, 0};
+    for (int b0 = c0; b0 < c1; b0 += p.piece) {
+        const int b1 = c1 - b0 < p.piece ? c1 : b0 + p.piece;
+        stage(b0, b1);
+        // two rows at a time: a staged piece ends with a multiple of four, zeros past the last
+        const int rows = (b1 - b0 + 3) & ~3;
+        for (int r = 2 * rg; r < rows; r += 64) {
+            uint64_t a0, b0_, a1, b1_;
+            four(r, a0, b0_);
+            four(r + 1, a1, b1_);
+            float l0, h0, l1, h1;
+            f2_split(a0, l0, h0);
+            f2_split(a1, l1, h1);
+            top[0] = max3_abs(top[0], l0, l1);
+            top[1] = max3_abs(top[1], h0, h1);
+            f2_split(b0_, l0, h0);
+            f2_split(b1_, l1, h1);
+            top[2] = max3_abs(top[2], l0, l1);
+            top[3] = max3_abs(top[3], h0, h1);
+        }
+        if (!once) __syncthreads();   // the next piece goes where this one was
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        amax[i] = max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 8));
-        amax[i] = max(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], 16));
-        if (lane < 8) s_part[warp][cg + i] = amax[i];
+    for (int i = 0; i < 4; ++i) {
+        uint32_t m = __float_as_uint(top[i]) & 0x7fffffffu;
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (lane < 8) s_part[warp][cg + i] = m;
     }
     __syncthreads();
     if (threadIdx.x < kI8FilterCols) {
@@ -87,52 +141,106 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
     }
     __syncthreads();
     cluster_sync_all();
-    I8RowScale sc[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    if (threadIdx.x < kI8FilterCols) {   // a column a thread: the CTAs' maxima, eight remote loads at once
         uint32_t m = 0;
-        for (uint32_t r = 0; r < S; ++r) {
+#pragma unroll
+        for (uint32_t r = 0; r < 8; ++r) {
             uint32_t v;
-            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_rank(smem_u32(&s_max[cg + i]), r)));
+            asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_rank(smem_u32(&s_max[threadIdx.x]), r < S ? r : 0u)));
             m = max(m, v);
         }
+        s_part[0][threadIdx.x] = m;
+    }
+    __syncthreads();
+    I8RowScale sc[4];
+    bool plain = true;   // no column of zeros, tiny, huge or not finite
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t m = s_part[0][cg + i];
         const bool finite = m < 0x7f800000u;
         sc[i] = i8_row_scale(m, finite);
+        plain = plain && !sc[i].dead && sc[i].up == 1.0f;
         const int o = o0 + cg + i;
         if (rank == 0 && threadIdx.x < 8 && o < p.Cout && in_bounds(o, 1, p.Cout, kSiteI8FilterScale, status))
             p.scale[o] = finite ? __uint_as_float(m) / 127.0f : __uint_as_float(0x7fc00000u);
     }
     cluster_sync_all();   // nobody leaves while its maxima may still be read
 
-    // Transposed tiles of 128 rows x 64 columns: a thread rounds 4 neighbouring rows of its eight
-    // columns to eight words along the rows.
-    for (int t0 = c0; t0 < c1; t0 += kI8FilterRows) {
-        const int rg = warp * 4 + (lane >> 3);   // row group: rows 4 rg .. 4 rg + 3 of the tile
-        uint32_t words[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        float v[4][8];
+    // bf16: the two sides of inv (i8_rows.cuh); float32: inv
+    constexpr bool BF16 = sizeof(T) == 2;
+    uint64_t inv0[2], inv1[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load(t0 + rg * 4 + j, v[j]);
+    for (int i = 0; i < 2; ++i) {
+        const float a = sc[2 * i].inv, b = sc[2 * i + 1].inv;
+        inv0[i] = BF16 ? f2_pack(a * kI8Below, b * kI8Below) : f2_pack(a, b);
+        inv1[i] = f2_pack(a * kI8Above, b * kI8Above);
+    }
+    const uint64_t magic = f2_pack(kI8Magic, kI8Magic), minus1 = f2_pack(-1.0f, -1.0f);
+    for (int b0 = c0; b0 < c1; b0 += p.piece) {
+        const int b1 = c1 - b0 < p.piece ? c1 : b0 + p.piece;
+        if (!once) stage(b0, b1);
+        const int groups = (b1 - b0 + 3) / 4;
+        for (int g = rg; g < groups; g += 32) {
+            uint32_t m[4][4];
+            float worst = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+            for (int j = 0; j < 4; ++j) {
+                uint64_t t[2];
+                four(g * 4 + j, t[0], t[1]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) words[i] |= (i8_quant1(v[j][i], sc[i]) & 0xffu) << (8 * j);
+                for (int i = 0; i < 2; ++i) {
+                    const uint64_t u = f2_fma(t[i], inv0[i], magic);
+                    float lo, hi, lo1, hi1;
+                    f2_split(u, lo, hi);
+                    if constexpr (BF16) {
+                        f2_split(f2_fma(t[i], inv1[i], magic), lo1, hi1);
+                        m[j][2 * i] = i8_even(lo, lo1);
+                        m[j][2 * i + 1] = i8_even(hi, hi1);
+                    } else {
+                        f2_split(f2_fma(t[i], inv0[i], f2_fma(u, minus1, magic)), lo1, hi1);
+                        worst = max3_abs(worst, lo1, hi1);
+                        m[j][2 * i] = __float_as_uint(lo);
+                        m[j][2 * i + 1] = __float_as_uint(hi);
+                    }
+                }
+            }
+            if (!plain || (!BF16 && worst > kI8NearHalf)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t settled = i8_quant1(i8_to_float(slab[(g * 4 + j) * kI8FilterCols + cg + i]), sc[i]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k == j) m[k][i] = settled;
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // rows 4 g .. 4 g + 3 of the column: word g, in chunk g / 4 of its 128-byte run, permuted
+                const int col = cg + i;
+                const int at = (g & ~31) * 4 + ((((g >> 2) & 7) ^ (col >> 2)) << 4) + (g & 3) * 4;
+                *reinterpret_cast<uint32_t *>(tile + static_cast<size_t>(col) * p.piece + at) =
+                    i8_bytes(m[0][i], m[1][i], m[2][i], m[3][i]);
+            }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<uint32_t *>(&s_tile[(cg + i) * kI8FilterPitch + rg * 4]) = words[i];
         __syncthreads();
-        // 64 columns x 128 bytes, a word a thread (a column's 128 bytes by one warp)
-        for (int w = threadIdx.x; w < kI8FilterCols * (kI8FilterRows / 4); w += 256) {
-            const int col = w >> 5, c = t0 + (w & 31) * 4, o = o0 + col;
-            if (o >= p.Cout || c >= c1) continue;
-            const uint32_t val = *reinterpret_cast<const uint32_t *>(&s_tile[col * kI8FilterPitch + (w & 31) * 4]);
+        const int chunks = (b1 - b0 + 15) / 16;
+        for (int i = threadIdx.x; i < kI8FilterCols * chunks; i += 256) {
+            const int col = i / chunks, j = i - col * chunks, o = o0 + col, c = b0 + j * 16;
+            if (o >= p.Cout) break;
+            const uint4 v = *reinterpret_cast<const uint4 *>(tile + static_cast<size_t>(col) * p.piece + (j & ~7) * 16 +
+                                                             (((j & 7) ^ (col >> 2)) << 4));
             int8_t *dst = p.q + 1LL * o * p.ldq + c;
-            if (c + 4 <= c1) {
-                if (in_bounds(1LL * o * p.Cin + c, 4, q_elems, kSiteI8FilterQ, status)) *reinterpret_cast<uint32_t *>(dst) = val;
+            const int n = b1 - c < 16 ? b1 - c : 16;
+            if (!in_bounds(1LL * o * p.Cin + c, n, q_elems, kSiteI8FilterQ, status)) continue;
+            if (n == 16) {
+                *reinterpret_cast<uint4 *>(dst) = v;
             } else {
-                for (int j = 0; j < c1 - c; ++j)
-                    if (in_bounds(1LL * o * p.Cin + c + j, 1, q_elems, kSiteI8FilterQ, status))
-                        dst[j] = static_cast<int8_t>(val >> (8 * j));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 15; ++k)
+                    if (k < n) dst[k] = static_cast<int8_t>(w[k >> 2] >> (8 * (k & 3)));
             }
         }
         __syncthreads();

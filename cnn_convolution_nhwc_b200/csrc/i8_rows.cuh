@@ -11,11 +11,13 @@
 // that are still in registers. A row is therefore read once and written once; the kernels are
 // bound by HBM bandwidth.
 //
-// Rounding is that of the real quotient 127 v / A of the float32 values v and A: the float32
-// product v * (127 / A) is off by at most 127 * 2^-23 < 2e-5, so only a product within 4e-5 of
-// a half can round to the wrong side, and those few are decided in float64, where 127 v and
-// (k + 1/2) A are exact (7 + 24 and 8 + 24 bits). The result does not depend on how a row is
-// divided among threads.
+// Rounding is that of the real quotient 127 v / A of the float32 values v and A, so the result does
+// not depend on how a row is divided among threads. inv = 127 / A is off by 2^-24 relative, so
+// v * inv can only round to the wrong side near a half; there the sign of 127 v - (k + 1/2) A is
+// taken exactly (a product's rounded part and its error, and two fused multiply-adds). Where v and
+// A are bf16 values, exact halves are common (about one value in 300) and nothing else comes
+// nearer to a half than 1.5e-5 relative: there v * inv (1 - 2^-20) and v * inv (1 + 2^-20) round
+// apart on exact halves only, and the even one is taken, without a branch.
 //
 // A row with A = 0 has q = 0 and scale = 0. A row that holds a NaN or an infinity (after the
 // gate, the residual and the weight), or whose sum of squares passes the float32 range, has
@@ -145,8 +147,9 @@ __device__ __forceinline__ float i8_glu(float a, float b) {
     return __fdividef(a < 0.0f ? a * e : a, 1.0f + e) * b;
 }
 
-// What one row's rounding needs: inv = 127 / (A * up), with `up` a power of two that brings rows
-// of tiny values (A < 2^-100, where 127 / A could overflow) into range exactly.
+// What one row's rounding needs: inv = 127 / (A * up), with `up` a power of two that brings rows of
+// tiny or huge values, where 127 / A or 127 v could leave the float32 range, back into it. The
+// scaling is exact but for values that become denormal, which are 2^-100 of A and round to 0.
 struct I8RowScale {
     float A, inv, up;
     bool dead;   // nothing to round: A = 0, or not finite
@@ -155,78 +158,94 @@ struct I8RowScale {
 __device__ __forceinline__ I8RowScale i8_row_scale(uint32_t amax_bits, bool finite) {
     I8RowScale s;
     s.dead = amax_bits == 0u || !finite;
-    s.up = amax_bits < 0x0d800000u ? 0x1p+60f : 1.0f;   // 0x0d800000 = 2^-100
+    // 0x0d800000 = 2^-100, 0x71800000 = 2^100
+    s.up = amax_bits < 0x0d800000u ? 0x1p+60f : amax_bits > 0x71800000u ? 0x1p-60f : 1.0f;
     s.A = __uint_as_float(amax_bits) * s.up;
     s.inv = s.dead ? 0.0f : 127.0f / s.A;
     return s;
 }
 
 constexpr float kI8Magic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
-constexpr float kI8NearHalf = 0.49996f;
+constexpr float kI8NearHalf = 0.49996f;   // 4e-5 off a half: v * inv is off by at most 127 * 2^-24 < 8e-6
+constexpr float kI8Below = 1.0f - 0x1p-20f, kI8Above = 1.0f + 0x1p-20f;
 
-// The nearest integer of 127 t / A where t * inv lies near a half.
-__device__ __noinline__ float i8_round_near_half(float t, float A, float inv) {
-    const float lo = floorf(t * inv);
-    const double have = static_cast<double>(t) * 127.0, half = (static_cast<double>(lo) + 0.5) * static_cast<double>(A);
-    if (have > half) return lo + 1.0f;
-    if (have < half) return lo;
-    return (static_cast<int>(lo) & 1) ? lo + 1.0f : lo;
+// The integer m = kI8Magic + k, k the nearest to v * inv, made the nearest to 127 v / A. With `side`
+// the sign of v * inv - k, k moves by `side` if side * (127 v - (k + side / 2) A) > 0, or = 0 and k
+// is odd. p and e hold 127 v exactly; near a half p and (k + side / 2) A agree in their leading 15
+// bits and more, so the first fused multiply-add is exact and the last sum has the exact sign.
+// Away from a half nothing moves.
+__device__ __forceinline__ uint32_t i8_settle(float v, float m, const I8RowScale &s) {
+    const float k = m - kI8Magic;
+    const float side = fmaf(v, s.inv, -k) > 0.0f ? 1.0f : -1.0f;
+    const float p = v * 127.0f, e = fmaf(v, 127.0f, -p);
+    const float d = side * (fmaf(-fmaf(side, 0.5f, k), s.A, p) + e);
+    const bool move = d > 0.0f || (d == 0.0f && (__float_as_uint(m) & 1u));
+    return __float_as_uint(move ? m + side : m);
 }
 
 // Rounds one value (the low byte of the result).
 __device__ __forceinline__ uint32_t i8_quant1(float t, const I8RowScale &s) {
     const float v = s.dead ? 0.0f : t * s.up;
-    float m = fmaf(v, s.inv, kI8Magic);
-    if (fabsf(fmaf(v, s.inv, kI8Magic - m)) > kI8NearHalf) m = i8_round_near_half(v, s.A, s.inv) + kI8Magic;
-    return __float_as_uint(m);
+    return i8_settle(v, fmaf(v, s.inv, kI8Magic), s);
+}
+
+// The even one of two neighbouring integers, or the common value of two equal ones.
+__device__ __forceinline__ uint32_t i8_even(float a, float b) {
+    const uint32_t u = __float_as_uint(a);
+    return (u & 1u) ? __float_as_uint(b) : u;
+}
+
+// The low bytes of four words.
+__device__ __forceinline__ uint32_t i8_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
 // Rounds eight values of a live row, already times `up`, to eight bytes (byte i of the pair of
-// words is value i).
+// words is value i). BF16: the values are bf16 values.
+template <bool BF16>
 __device__ __forceinline__ uint2 i8_quant8(const uint64_t (&t)[4], const I8RowScale &s) {
-    const uint64_t inv = f2_pack(s.inv, s.inv), magic = f2_pack(kI8Magic, kI8Magic), minus1 = f2_pack(-1.0f, -1.0f);
-    uint64_t m[4];
-    float worst = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        m[i] = f2_fma(t[i], inv, magic);
-        const uint64_t off = f2_fma(t[i], inv, f2_fma(m[i], minus1, magic));   // t * inv less the integer
-        float lo, hi;
-        f2_split(off, lo, hi);
-        worst = max3_abs(worst, lo, hi);
-    }
+    const uint64_t magic = f2_pack(kI8Magic, kI8Magic);
     uint32_t b[8];
+    if constexpr (BF16) {
+        const float below = s.inv * kI8Below, above = s.inv * kI8Above;
+        const uint64_t inv0 = f2_pack(below, below), inv1 = f2_pack(above, above);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float lo, hi;
-        f2_split(m[i], lo, hi);
-        b[2 * i] = __float_as_uint(lo);
-        b[2 * i + 1] = __float_as_uint(hi);
-    }
-    if (worst > kI8NearHalf) {
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {
-            // selected by constant indices, so that the arrays stay in registers
-            float v = 0.0f;
-            uint32_t have = 0;
+        for (int i = 0; i < 4; ++i) {
+            float lo0, hi0, lo1, hi1;
+            f2_split(f2_fma(t[i], inv0, magic), lo0, hi0);
+            f2_split(f2_fma(t[i], inv1, magic), lo1, hi1);
+            b[2 * i] = i8_even(lo0, lo1);
+            b[2 * i + 1] = i8_even(hi0, hi1);
+        }
+    } else {
+        const uint64_t inv = f2_pack(s.inv, s.inv), minus1 = f2_pack(-1.0f, -1.0f);
+        uint64_t m[4];
+        float worst = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < 4; ++i) {
+            m[i] = f2_fma(t[i], inv, magic);
+            float lo, hi;
+            f2_split(f2_fma(t[i], inv, f2_fma(m[i], minus1, magic)), lo, hi);   // t * inv less the integer
+            worst = max3_abs(worst, lo, hi);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            f2_split(m[i], lo, hi);
+            b[2 * i] = __float_as_uint(lo);
+            b[2 * i + 1] = __float_as_uint(hi);
+        }
+        if (worst > kI8NearHalf) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
                 float lo, hi;
-                f2_split(t[j], lo, hi);
-                if (i == 2 * j) { v = lo; have = b[2 * j]; }
-                if (i == 2 * j + 1) { v = hi; have = b[2 * j + 1]; }
-            }
-            if (fabsf(fmaf(v, s.inv, kI8Magic - __uint_as_float(have))) > kI8NearHalf) {
-                have = __float_as_uint(i8_round_near_half(v, s.A, s.inv) + kI8Magic);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (i == j) b[j] = have;
+                f2_split(t[i], lo, hi);
+                b[2 * i] = i8_settle(lo, __uint_as_float(b[2 * i]), s);
+                b[2 * i + 1] = i8_settle(hi, __uint_as_float(b[2 * i + 1]), s);
             }
         }
     }
-    const uint32_t lo = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
-    const uint32_t hi = __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410);
-    return make_uint2(lo, hi);
+    return make_uint2(i8_bytes(b[0], b[1], b[2], b[3]), i8_bytes(b[4], b[5], b[6], b[7]));
 }
 
 // One row per group of threads: a warp (TPR = 32) or a block. A thread holds NV groups of eight
@@ -245,6 +264,7 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
     grid_dependency_wait();
     constexpr bool NORM = MODE == kI8Norm || MODE == kI8NormResidual;
     constexpr bool GROUP_WARP = TPR == 32;
+    constexpr bool BF16 = MODE == kI8Plain && sizeof(T) == 2;   // the rounded values are bf16 values
     __shared__ float s_sum[16];
     __shared__ uint32_t s_max[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -423,7 +443,7 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t[k][i] = f2_mul(t[k][i], f2_pack(s.up, s.up));
             }
-            store(c0, k, s.dead ? make_uint2(0u, 0u) : i8_quant8(t[k], s));
+            store(c0, k, s.dead ? make_uint2(0u, 0u) : i8_quant8<BF16>(t[k], s));
         }
         if (C - c0 <= piece) break;
     }

@@ -142,7 +142,7 @@ def test_special_rows(cb, C, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("Cin,Cout", [(1, 1), (7, 3), (64, 64), (128, 72), (129, 65), (250, 8), (1000, 1353), (1024, 512),
-                                      (1025, 200), (4100, 136), (5003, 33)])
+                                      (1025, 200), (4100, 136), (5003, 33), (9000, 72), (9100, 65), (17000, 40), (10300, 33)])
 def test_quant_filter(cb, Cin, Cout, dtype):
     g = _gen(Cin, Cout)
     F = _normal(g, Cin, Cout, dtype=dtype)
