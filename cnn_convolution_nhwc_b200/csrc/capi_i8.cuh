@@ -148,13 +148,13 @@ int launch_i8_pair(const I8Operands &a, I8GemmParams p, cudaStream_t stream, Dev
     CUtensorMap tmQ, tmW, tmY;
     if (int rc = i8_map(&tmQ, a.q, p.M, a.Cin, a.ldq, 128)) return rc;
     if (int rc = i8_map(&tmW, a.Wq, p.N, a.Cin, a.ldw, Cfg::BN / 2)) return rc;
-    if (p.vec) {   // Y in boxes of 32 rows x 128 bytes
+    if (p.vec) {   // Y in boxes of 32 rows x 64 bytes
         const cuuint64_t dims[2] = {(cuuint64_t)p.N, (cuuint64_t)p.M};
         const cuuint64_t strides[1] = {(cuuint64_t)p.N * sizeof(OUT)};
-        const cuuint32_t box[2] = {128 / (cuuint32_t)sizeof(OUT), 32};
+        const cuuint32_t box[2] = {64 / (cuuint32_t)sizeof(OUT), 32};
         const cuuint32_t estr[2] = {1, 1};
         if (g_encode_tiled(&tmY, sizeof(OUT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-                           p.Y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           p.Y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return CONV_ERR_CUDA;
     } else {

@@ -263,17 +263,23 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 // of the accumulator. Two accumulators, so tile t + 1 multiplies while tile t is scaled and stored.
 //   warp 0      TMA ring of STAGES slots
 //   warp 1      TMEM allocation; the even CTA's issues the MMAs for both
-//   warps 2..9  epilogue, two warps per TMEM lane quarter taking alternate chunks of 128 bytes of
-//               output: tcgen05.ld, scale, round, swizzled staging, one tensor store a chunk. A
-//               warp fetches its columns' scales and biases into its own corner of shared memory
-//               before it waits for the accumulator, so their latency hides behind the MMAs.
+//   warps 2..17 epilogue, four warps per TMEM lane quarter with a quarter of the columns each, in
+//               units of 64 bytes of output a row: tcgen05.ld, scale, round, swizzled staging, one
+//               tensor store a unit. A warp has its columns' scales and biases fetched a tile ahead
+//               and staged in its own corner of shared memory. With short reductions the epilogue
+//               is the bound: 25088 x 512 outputs of 256 terms take 5.1 us without it, 11.6 us with
+//               it. Its loop is kept short: unrolled over a tile's units, or with a second form of
+//               the conversions, it takes 13 to 16 us, since a launch runs each instruction a few
+//               times only and waits for the instruction cache.
 template <int BN_, int STAGES_>
 struct I8PairCfg {
     static constexpr int BN = BN_, STAGES = STAGES_;   // per CTA: 128 rows; the pair: 256
+    static constexpr int NUM_EPI = 16;
+    static constexpr int UNIT_BYTES = 32 * 64;           // staging of an epilogue warp: 64 bytes a row
     static constexpr int A_BYTES = 128 * 128, B_BYTES = BN / 2 * 128, SLOT = A_BYTES + B_BYTES;
-    static constexpr int NUM_EPI = 8;
-    static constexpr int EPI_BYTES = NUM_EPI * 32 * 128;
-    static constexpr int SCALE_BYTES = NUM_EPI * (BN / 2) * 8;   // a warp's columns: scale, bias
+    static constexpr int EPI_BYTES = NUM_EPI * UNIT_BYTES;
+    static constexpr int COLS = BN / 4;                  // columns of an epilogue warp
+    static constexpr int SCALE_BYTES = NUM_EPI * COLS * 8;   // their scales and biases
     static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
     static constexpr int SMEM = 1024 + STAGES * SLOT + EPI_BYTES + SCALE_BYTES + NUM_BARS * 8 + 16;
     static constexpr int THREADS = 32 * (2 + NUM_EPI);
@@ -406,15 +412,34 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (!mbar_wait_warp(done_bar, 0) && lane == 0) fail();
         }
     } else {
-        constexpr int CW = 128 / static_cast<int>(sizeof(OUT));   // columns of a 128-byte chunk
+        constexpr int UW = 64 / static_cast<int>(sizeof(OUT));    // columns of a unit
+        constexpr int UNITS = Cfg::COLS / UW;
         constexpr int V = 16 / static_cast<int>(sizeof(OUT));     // values of 16 bytes
-        constexpr int CHUNKS = Cfg::BN / CW / 2;                  // chunks a warp takes: eg, eg + 2, ...
         const int quarter = warp & 3, eg = (warp - 2) >> 2;
-        const uint32_t stage = base + epi_off + (warp - 2) * 4096;
-        float *s_ws = reinterpret_cast<float *>(smem + scale_off) + (warp - 2) * Cfg::BN;   // CHUNKS x CW scales,
-        float *s_bias = s_ws + Cfg::BN / 2;                                                  // then biases
+        const uint32_t stage = base + epi_off + (warp - 2) * Cfg::UNIT_BYTES;
+        float *s_ws = reinterpret_cast<float *>(smem + scale_off) + (warp - 2) * 2 * Cfg::COLS;   // scales, then biases
+        float *s_bias = s_ws + Cfg::COLS;
         OUT *Y = static_cast<OUT *>(p.Y);
         const long long y_elems = 1LL * p.M * p.N;
+        auto swizzle = [](int row) { return (row >> 1) & 3; };   // of the 16-byte pieces of a 64-byte row
+        const uint32_t leader = elect_one_sync();
+        // The scales of a tile: the lane's row, and the warp's columns 32 at a time. They are fetched a
+        // tile ahead.
+        float qs_next = 0.0f, ws_next[Cfg::COLS / 32], bias_next[Cfg::COLS / 32];
+        auto fetch = [&](int t) {
+            int mt, nt;
+            i8_tile(t, p.m_tiles, p.n_tiles, mt, nt);
+            const int row = mt * 256 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+            qs_next = row < p.M && in_bounds(row, 1, p.M, kSiteI8GemmScale, status) ? p.q_scale[row] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < Cfg::COLS / 32; ++i) {
+                const int c = nt * Cfg::BN + eg * Cfg::COLS + i * 32 + lane;
+                const bool in = c < p.N && in_bounds(c, 1, p.N, kSiteI8GemmScale, status);
+                ws_next[i] = in ? p.w_scale[c] : 0.0f;
+                bias_next[i] = in && p.bias ? p.bias[c] : 0.0f;
+            }
+        };
+        if (first < p.num_tiles) fetch(first);
         uint32_t local = 0;
         for (int t = first; t < p.num_tiles; t += step, ++local) {
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
@@ -422,85 +447,93 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             int mt, nt;
             i8_tile(t, p.m_tiles, p.n_tiles, mt, nt);
             const int row0 = mt * 256 + static_cast<int>(rank) * 128 + quarter * 32;   // this warp's 32 rows
-            const int n0 = nt * Cfg::BN;
-            const float qs = row0 + lane < p.M && in_bounds(row0 + lane, 1, p.M, kSiteI8GemmScale, status)
-                                 ? p.q_scale[row0 + lane] : 0.0f;
+            const int n0 = nt * Cfg::BN + eg * Cfg::COLS;                              // its columns
+            const uint64_t qs = f2_pack(qs_next, qs_next);
+            __syncwarp();   // the previous tile's scales have been read
 #pragma unroll
-            for (int i = 0; i < Cfg::BN / 64; ++i) {   // the warp's BN / 2 columns, 32 at a time
-                const int e = i * 32 + lane, c = n0 + (2 * (e / CW) + eg) * CW + e % CW;
-                const bool in = c < p.N && in_bounds(c, 1, p.N, kSiteI8GemmScale, status);
-                s_ws[e] = in ? p.w_scale[c] : 0.0f;
-                s_bias[e] = in && p.bias ? p.bias[c] : 0.0f;
+            for (int i = 0; i < Cfg::COLS / 32; ++i) {
+                s_ws[i * 32 + lane] = ws_next[i];
+                s_bias[i * 32 + lane] = bias_next[i];
             }
             __syncwarp();
+            if (t + step < p.num_tiles) fetch(t + step);
             if (!mbar_wait_backoff(accf(b), (local >> 1) & 1u, 32)) { if (lane == 0) fail(); break; }
             tc_fence_after();
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * Cfg::BN;
+            const uint32_t t_row =
+                tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + b * Cfg::BN + eg * Cfg::COLS;
 #pragma unroll 1
-            for (int k = 0; k < CHUNKS; ++k) {
-                const int h = 2 * k + eg, c0 = n0 + h * CW;
-                uint32_t r[CW / 16][16];
+            for (int u = 0; u < UNITS; ++u) {
+                const int c0 = n0 + u * UW;
+                uint32_t r[UW];
 #pragma unroll
-                for (int g = 0; g < CW / 16; ++g) tmem_ld_32x32b_x16(t_row + h * CW + g * 16, r[g]);
+                for (int g = 0; g < UW / 16; ++g)
+                    tmem_ld_32x32b_x16(t_row + u * UW + g * 16, *reinterpret_cast<uint32_t(*)[16]>(r + g * 16));
                 tmem_wait_ld();
-                if (k == CHUNKS - 1) {   // the accumulator is read: the next tile but one may overwrite it
+                if (u + 1 == UNITS) {   // the accumulator is read: the next tile but one may have it
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(lead(acce(b)));
+                    mbar_arrive_cluster_if(lead(acce(b)), leader);
                 }
-                uint32_t packed[32];   // the lane's 128 bytes
+                uint64_t v[UW / 2];
 #pragma unroll
-                for (int g = 0; g < CW / 4; ++g) {
-                    const float4 w = *reinterpret_cast<const float4 *>(s_ws + k * CW + g * 4);
-                    const uint32_t *a = &r[g / 4][(g % 4) * 4];
-                    float v[4] = {static_cast<float>(static_cast<int>(a[0])) * qs * w.x,
-                                  static_cast<float>(static_cast<int>(a[1])) * qs * w.y,
-                                  static_cast<float>(static_cast<int>(a[2])) * qs * w.z,
-                                  static_cast<float>(static_cast<int>(a[3])) * qs * w.w};
-                    if (p.bias) {
-                        const float4 bb = *reinterpret_cast<const float4 *>(s_bias + k * CW + g * 4);
-                        v[0] += bb.x; v[1] += bb.y; v[2] += bb.z; v[3] += bb.w;
-                    }
-                    if constexpr (sizeof(OUT) == 2) {
-                        packed[2 * g] = halo_pack_bf16x2(v[0], v[1]);
-                        packed[2 * g + 1] = halo_pack_bf16x2(v[2], v[3]);
-                    } else {
+                for (int i = 0; i < UW / 2; ++i)
+                    v[i] = f2_pack(static_cast<float>(static_cast<int>(r[2 * i])), static_cast<float>(static_cast<int>(r[2 * i + 1])));
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) packed[4 * g + i] = __float_as_uint(v[i]);
+                for (int i = 0; i < UW / 4; ++i) {
+                    const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(s_ws + u * UW + i * 4);
+                    v[2 * i] = f2_mul(f2_mul(v[2 * i], qs), w.x);
+                    v[2 * i + 1] = f2_mul(f2_mul(v[2 * i + 1], qs), w.y);
+                }
+                if (p.bias) {
+#pragma unroll
+                    for (int i = 0; i < UW / 4; ++i) {
+                        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(s_bias + u * UW + i * 4);
+                        v[2 * i] = f2_add(v[2 * i], w.x);
+                        v[2 * i + 1] = f2_add(v[2 * i + 1], w.y);
                     }
                 }
-                if (p.vec && lane == 0) bulk_wait_group_read0();   // the previous chunk has left the staging
+                bulk_wait_group_read0();   // the previous unit has left the staging (the leader's store)
                 __syncwarp();
+                // 16-byte pieces of the lane's 64-byte row, 64-byte swizzle
 #pragma unroll
-                for (int c = 0; c < 8; ++c)   // 16-byte piece c of the lane's row, 128-byte swizzle
-                    st_shared_v4(stage + lane * 128 + ((c ^ (lane & 7)) << 4), packed[4 * c], packed[4 * c + 1],
-                                 packed[4 * c + 2], packed[4 * c + 3]);
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        float lo, hi;
+                        if constexpr (sizeof(OUT) == 2) {
+                            f2_split(v[4 * c + j], lo, hi);
+                            o[j] = halo_pack_bf16x2(lo, hi);
+                        } else {
+                            f2_split(v[2 * c + j / 2], lo, hi);
+                            o[j] = __float_as_uint(j & 1 ? hi : lo);
+                        }
+                    }
+                    st_shared_v4(stage + lane * 64 + ((c ^ swizzle(lane)) << 4), o[0], o[1], o[2], o[3]);
+                }
                 if (p.vec) {
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0 && c0 < p.N && row0 < p.M) {   // rows and columns past Y are not stored
-                        tma_store_2d(&tmY, stage, c0, row0);
-                        bulk_commit_group();
-                    }
-                } else {   // rows of Y off the 16-byte boundaries: an element a lane, a row at a time
+                    // rows and columns past Y are not stored
+                    tma_store_2d_commit_if(&tmY, stage, c0, row0, c0 < p.N && row0 < p.M ? leader : 0u);
+                } else {   // rows of Y off the 16-byte boundaries: an element a lane
                     __syncwarp();
+                    const uint8_t *from = smem + (stage - base);
                     const int rows = p.M - row0 < 32 ? p.M - row0 : 32;
+                    constexpr int RPI = 32 / UW;   // rows an instruction
+                    const int e = lane % UW, col = c0 + e;
 #pragma unroll 4
-                    for (int rr = 0; rr < rows; ++rr) {
-#pragma unroll
-                        for (int i = 0; i < CW / 32; ++i) {
-                            const int e = i * 32 + lane, col = c0 + e;
-                            const long long at = 1LL * (row0 + rr) * p.N + col;
-                            if (col < p.N && in_bounds(at, 1, y_elems, kSiteI8GemmY, status))
-                                Y[at] = *reinterpret_cast<const OUT *>(
-                                    smem + epi_off + (warp - 2) * 4096 + rr * 128 + (((e / V) ^ (rr & 7)) << 4) +
-                                    (e % V) * sizeof(OUT));
-                        }
+                    for (int rr = lane / UW; rr < rows; rr += RPI) {
+                        const long long at = 1LL * (row0 + rr) * p.N + col;
+                        if (col < p.N && in_bounds(at, 1, y_elems, kSiteI8GemmY, status))
+                            Y[at] = *reinterpret_cast<const OUT *>(from + rr * 64 + (((e / V) ^ swizzle(rr)) << 4) +
+                                                                   (e % V) * sizeof(OUT));
                     }
+                    __syncwarp();
                 }
             }
         }
-        if (lane == 0) bulk_wait_group0();   // the stores are complete before the CTA exits
+        bulk_wait_group_read0();   // the stores have left shared memory before the CTA exits
     }
 
     tc_fence_before();

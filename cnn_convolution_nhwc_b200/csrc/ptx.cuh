@@ -331,6 +331,25 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, uint32_t src,
                  : "memory");
 }
 
+// A tensor store and its bulk group by the lane whose `leader` is non-zero, in a converged warp.
+__device__ __forceinline__ void tma_store_2d_commit_if(const CUtensorMap *m, uint32_t src, int x, int y, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n\t"
+        "@q cp.async.bulk.commit_group;\n\t}"
+        :
+        : "l"(reinterpret_cast<uint64_t>(m)), "r"(src), "r"(x), "r"(y), "r"(leader)
+        : "memory");
+}
+
+// mbar_arrive_cluster by the lane whose `leader` is non-zero, in a converged warp.
+__device__ __forceinline__ void mbar_arrive_cluster_if(uint32_t addr, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(addr), "r"(leader)
+        : "memory");
+}
+
 __device__ __forceinline__ void bulk_commit_group() {
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
