@@ -408,62 +408,77 @@ def dwpw_fwd(x, w_dw, b_dw, F, b_pw=None, y=None, stride=1, pad=0, dil=1, mode=D
 
 # ---- 8-bit operators ---------------------------------------------------------------------
 # Their single-token calls take a few microseconds on the GPU, so these wrappers keep to a few on
-# the host: one test per tensor on the good path (the messages come from _tensor), and the device
-# switched only when it is not the current one.
+# the host: one test per tensor on the good path (the messages come from the slow one), torch looked
+# up once, and the device switched only when it is not the current one.
+_BF16 = _F32 = _INT8 = _raw_stream = _current_device = None
+
+
+def _i8_init():
+    global _BF16, _F32, _INT8, _raw_stream, _current_device
+    import torch
+    _BF16, _F32, _INT8 = torch.bfloat16, torch.float32, torch.int8
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _i8_matrix(x, name):
+    """(conv_dtype, address) of a contiguous bfloat16 or float32 CUDA matrix."""
+    import torch
+    if _BF16 is None:
+        _i8_init()
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype is not _BF16 and x.dtype is not _F32:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {x.dtype}")
+    _tensor(x, x.dtype, 2, name)
+    return CONV_BF16 if x.dtype is _BF16 else CONV_F32, x.data_ptr()
 
 
 def _i8_ptr(t, dtype, shape, name):
     """The address of a contiguous CUDA tensor of the given type and shape."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _tensor(t, dtype, len(shape), name)
     raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _i8_conv_dtype(t, name):
-    """The conv_dtype of a bfloat16 or float32 tensor."""
+def _i8_rows(t, name):
+    """(address, rows, columns, row pitch) of an int8 matrix whose rows start on 16-byte boundaries."""
+    try:
+        if t.dtype is _INT8 and t.is_cuda:
+            n, c = t.shape
+            pitch, step = t.stride()
+            if n < 2:
+                pitch = (c + 15) & ~15   # the stride of a dimension with one element means nothing
+            if (step == 1 or c < 2) and pitch >= c and not pitch & 15:
+                return t.data_ptr(), n, c, pitch
+    except (AttributeError, ValueError):
+        pass
     import torch
-    if isinstance(t, torch.Tensor):
-        if t.dtype is torch.bfloat16:
-            return CONV_BF16
-        if t.dtype is torch.float32:
-            return CONV_F32
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    raise TypeError(f"{name} must be a torch.Tensor")
-
-
-def _i8_rows(t, name, rows=None, C=None):
-    """(address, row pitch) of an int8 matrix whose rows start on 16-byte boundaries."""
-    import torch
+    if _INT8 is None:
+        _i8_init()
+        return _i8_rows(t, name)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not torch.int8:
+    if t.dtype is not _INT8:
         raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
-    n, c = t.shape
-    if (rows is not None and n != rows) or (C is not None and c != C):
-        raise ValueError(f"{name} must have shape {(rows if rows is not None else n, C if C is not None else c)}, got {(n, c)}")
-    pitch, step = t.stride()
-    if n < 2:
-        pitch = (c + 15) // 16 * 16   # the stride of a dimension with one element means nothing
-    if (step != 1 and c > 1) or pitch < c or pitch & 15:
-        raise ValueError(f"{name} must be an int8 matrix whose rows are contiguous and start on 16-byte boundaries "
-                         "(empty_rows_i8 makes one)")
-    return t.data_ptr(), pitch
+    raise ValueError(f"{name} must be an int8 matrix whose rows are contiguous and start on 16-byte boundaries "
+                     "(empty_rows_i8 makes one)")
 
 
-def _i8_call(fn, what, tensors, stream, *args):
-    """_call for the 8-bit entry points."""
-    import torch
-    index = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != index:
-            _device(*tensors)
-    if stream is None and index == torch._C._cuda_getDevice():
-        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+def _i8_call(fn, what, index, tensors, stream, *args):
+    """_call for the 8-bit entry points; `index`: the device of the first tensor."""
+    if stream is None and index == _current_device():
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                _device(*tensors)
+        rc = fn(*args, _raw_stream(index))
         if rc != CONV_OK:
             _check(rc, what)
     else:
@@ -488,25 +503,24 @@ def _i8_out(q, scale, rows, C, device):
         q = empty_rows_i8(rows, C, device)
     if scale is None:
         scale = torch.empty(rows, dtype=torch.float32, device=device)
-    pq, pitch = _i8_rows(q, "q", rows, C)
-    return q, scale, pq, pitch, _i8_ptr(scale, torch.float32, (rows,), "scale")
+    pq, n, c, pitch = _i8_rows(q, "q")
+    if n != rows or c != C:
+        raise ValueError(f"q must have shape {(rows, C)}, got {(n, c)}")
+    return q, scale, pq, pitch, _i8_ptr(scale, _F32, (rows,), "scale")
 
 
 def _i8_result(y, dtype, shape, device):
-    import torch
+    """y (allocated where None), its conv_dtype and its address."""
     if y is None:
-        return torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
-    if dtype is not None and y.dtype is not dtype:
+        import torch
+        y = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+    elif dtype is not None and y.dtype is not dtype:
         raise TypeError(f"y must be {dtype}, got {y.dtype}")
-    return y
-
-
-def _i8_matrix(x, name):
-    """(conv_dtype, address) of a contiguous bfloat16 or float32 CUDA matrix."""
-    dt = _i8_conv_dtype(x, name)
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
-        _tensor(x, x.dtype, 2, name)
-    return dt, x.data_ptr()
+    if y.dtype is _BF16:
+        return y, CONV_BF16, _i8_ptr(y, _BF16, shape, "y")
+    if y.dtype is _F32:
+        return y, CONV_F32, _i8_ptr(y, _F32, shape, "y")
+    raise TypeError(f"y must be torch.bfloat16 or torch.float32, got {y.dtype}")
 
 
 def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-6, stream=None):
@@ -515,20 +529,21 @@ def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-
     a residual), then h * weight / sqrt(mean(h^2) + eps) as int8 q [M, C] and float32 scale [M].
     weight is float32 [C]. h may be x or residual (updated in place). Returns (q, scale, h); h is
     None without a residual."""
-    import torch
     dt, px = _i8_matrix(x, "x")
-    M, C = x.shape
-    pw = _i8_ptr(weight, torch.float32, (C,), "weight")
+    shape = x.shape
+    M, C = shape
+    pw = _i8_ptr(weight, _F32, (C,), "weight")
     pr = ph = None
     if residual is not None:
-        pr = _i8_ptr(residual, x.dtype, x.shape, "residual")
+        pr = _i8_ptr(residual, x.dtype, shape, "residual")
         if h is None:
+            import torch
             h = torch.empty_like(x)
-        ph = _i8_ptr(h, x.dtype, x.shape, "h")
+        ph = _i8_ptr(h, x.dtype, shape, "h")
     elif h is not None:
         raise ValueError("h is x + residual: give the residual too")
     q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
-    _i8_call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", (x, residual, weight, h, q, scale), stream,
+    _i8_call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", x.get_device(), (residual, weight, h, q, scale, x), stream,
              px, pr, pw, ph, pq, ps, M, C, ldq, eps, dt)
     return q, scale, h
 
@@ -543,51 +558,47 @@ def quant_rows_i8_fwd(x, glu=False, q=None, scale=None, stream=None):
             raise ValueError("glu needs x [M, 2C]")
         C //= 2
     q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
-    _i8_call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", (x, q, scale), stream, px, pq, ps, M, C, ldq, 1 if glu else 0, dt)
+    _i8_call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", x.get_device(), (q, scale, x), stream,
+             px, pq, ps, M, C, ldq, 1 if glu else 0, dt)
     return q, scale
 
 
 def quant_filter_i8_fwd(F, q=None, scale=None, stream=None):
     """8-bit rows of a 1 x 1 filter F [Cin, Cout] or [1, 1, Cin, Cout] (bfloat16 or float32): int8
     q [Cout, Cin], transposed, and float32 scale [Cout], one per output channel. Returns (q, scale)."""
-    dt = _i8_conv_dtype(F, "F")
-    if F.dim() == 4 and tuple(F.shape[:2]) != (1, 1):
-        raise ValueError("F must be a 1 x 1 filter")
-    pf = _tensor(F, F.dtype, 4 if F.dim() == 4 else 2, "F")
-    Cin, Cout = F.shape[-2:]
+    if getattr(F, "ndim", 0) == 4:
+        if tuple(F.shape[:2]) != (1, 1):
+            raise ValueError("F must be a 1 x 1 filter")
+        F = F[0, 0]
+    dt, pf = _i8_matrix(F, "F")
+    Cin, Cout = F.shape
     q, scale, pq, ldw, ps = _i8_out(q, scale, Cout, Cin, F.device)
-    _i8_call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", (F, q, scale), stream, pf, pq, ps, Cin, Cout, ldw, dt)
+    _i8_call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", F.get_device(), (q, scale, F), stream,
+             pf, pq, ps, Cin, Cout, ldw, dt)
     return q, scale
 
 
 def dequant_rows_i8_fwd(q, scale, y=None, dtype=None, stream=None):
     """Reads 8-bit rows back: y [M, C] = q * scale, in y's type (dtype, bfloat16 by default)."""
-    import torch
-    pq, ldq = _i8_rows(q, "q")
-    M, C = q.shape
-    ps = _i8_ptr(scale, torch.float32, (M,), "scale")
-    y = _i8_result(y, dtype, (M, C), q.device)
-    dt = _i8_conv_dtype(y, "y")
-    py = _i8_ptr(y, y.dtype, (M, C), "y")
-    _i8_call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", (q, scale, y), stream, pq, ps, py, M, C, ldq, dt)
+    pq, M, C, ldq = _i8_rows(q, "q")
+    ps = _i8_ptr(scale, _F32, (M,), "scale")
+    y, dt, py = _i8_result(y, dtype, (M, C), q.device)
+    _i8_call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", q.get_device(), (scale, y, q), stream,
+             pq, ps, py, M, C, ldq, dt)
     return y
 
 
 def pointwise_i8_fwd(q, q_scale, Wq, w_scale, bias=None, y=None, dtype=None, stream=None):
     """The product of 8-bit rows: y [M, Cout] = (q [M, Cin] @ Wq [Cout, Cin]^T) * q_scale [M] * w_scale [Cout]
     + bias [Cout], the sum exact in int32, in y's type (dtype, bfloat16 by default)."""
-    import torch
-    pq, ldq = _i8_rows(q, "q")
-    M, Cin = q.shape
-    pw, ldw = _i8_rows(Wq, "Wq", None, Cin)
-    Cout = Wq.shape[0]
-    f32 = torch.float32
-    ps, pws = _i8_ptr(q_scale, f32, (M,), "q_scale"), _i8_ptr(w_scale, f32, (Cout,), "w_scale")
-    pb = None if bias is None else _i8_ptr(bias, f32, (Cout,), "bias")
-    y = _i8_result(y, dtype, (M, Cout), q.device)
-    dt = _i8_conv_dtype(y, "y")
-    py = _i8_ptr(y, y.dtype, (M, Cout), "y")
-    _i8_call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", (q, q_scale, Wq, w_scale, bias, y), stream,
+    pq, M, Cin, ldq = _i8_rows(q, "q")
+    pw, Cout, Cin2, ldw = _i8_rows(Wq, "Wq")
+    if Cin2 != Cin:
+        raise ValueError(f"Wq must have q's {Cin} columns, got {Cin2}")
+    ps, pws = _i8_ptr(q_scale, _F32, (M,), "q_scale"), _i8_ptr(w_scale, _F32, (Cout,), "w_scale")
+    pb = None if bias is None else _i8_ptr(bias, _F32, (Cout,), "bias")
+    y, dt, py = _i8_result(y, dtype, (M, Cout), q.device)
+    _i8_call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", q.get_device(), (q_scale, Wq, w_scale, bias, y, q), stream,
              pq, ps, pw, pws, pb, py, M, Cin, Cout, ldq, ldw, dt)
     return y
 
@@ -598,14 +609,14 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
     int8 [Cout, Cin] with w_scale [Cout] (quant_filter_i8_fwd) -> Y bfloat16 [N,H,W,Cout].
     workspace: a uint8 CUDA tensor of at least conv2d_nhwc_i8_workspace bytes, allocated here if None."""
     import torch
+    pw, Cout, Cin2, ldw = _i8_rows(Wq, "Wq")
     px = _tensor(X, torch.bfloat16, 4, "X")
     N, H, W, Cin = X.shape
-    pw, ldw = _i8_rows(Wq, "Wq", None, Cin)
-    Cout = Wq.shape[0]
-    f32 = torch.float32
-    pws = _i8_ptr(w_scale, f32, (Cout,), "w_scale")
-    pb = None if bias is None else _i8_ptr(bias, f32, (Cout,), "bias")
-    pn = None if norm is None else _i8_ptr(norm, f32, (Cin,), "norm")
+    if Cin2 != Cin:
+        raise ValueError(f"Wq must have X's {Cin} channels, got {Cin2}")
+    pws = _i8_ptr(w_scale, _F32, (Cout,), "w_scale")
+    pb = None if bias is None else _i8_ptr(bias, _F32, (Cout,), "bias")
+    pn = None if norm is None else _i8_ptr(norm, _F32, (Cin,), "norm")
     if workspace is None:
         need = lib.conv2d_nhwc_i8_workspace(N, H, W, Cin)
         if need == 0:
@@ -615,8 +626,8 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if Y is None:
         Y = torch.empty((N, H, W, Cout), dtype=torch.bfloat16, device=X.device)
-    py = _i8_ptr(Y, torch.bfloat16, (N, H, W, Cout), "Y")
-    _i8_call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", (X, norm, Wq, w_scale, bias, Y, workspace), stream,
+    py = _i8_ptr(Y, _BF16, (N, H, W, Cout), "Y")
+    _i8_call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", X.get_device(), (norm, Wq, w_scale, bias, Y, workspace, X), stream,
              px, pn, eps, pw, pws, pb, py, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
              N, H, W, Cin, Cout, ldw)
     return Y

@@ -2,6 +2,8 @@
 // end of capi.cu, whose helpers (device state, launch_k, pointer checks) it uses.
 #pragma once
 
+#include <cmath>
+
 namespace convb200 {
 namespace {
 
@@ -191,50 +193,102 @@ struct I8Plan {
     int bn, split;
 };
 
-I8Plan plan_i8(int M, int N, int num_kblk, int num_sms) {
-    I8Plan pl{true, 256, 1};
-    if (M <= 128) {
-        pl.pair = false;
-        pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-        const long long tiles = 1LL * ((N + 127) / 128) * ((M + pl.bn - 1) / pl.bn);
-        while (pl.split < 8 && tiles * pl.split * 2 <= num_sms && pl.split * 4 <= num_kblk) pl.split *= 2;
-    } else {
-        // half-width tiles while whole ones would leave half of the pairs idle
-        const long long tiles = 1LL * ((M + 255) / 256) * ((N + 255) / 256);
-        if (tiles * 4 <= num_sms) pl.bn = 128;
-    }
+// k blocks of a slot of the split kernel: two, but for the widest tile and where two CTAs share an SM.
+constexpr int i8_slot_kblks(int bn, bool shared) { return bn == 128 || shared ? 1 : 2; }
+
+// Picks the plan whose estimated time (us) is least. The estimate is a start (launch, first copy),
+// an epilogue per round of CTAs, and the larger-than-either sum (hypot) of the k loop and of the
+// bytes at HBM's rate; a k block takes its own time or what its copies take when every SM's go
+// through L2. The constants are a fit to 2200 measured times on a B200, M 1 .. 2048, N 1024 .. 20480,
+// Cin 512 .. 10240 (rms error 10 %; the plan it picks is on average 1 % slower than the best one
+// measured, the fixed rule it replaced 10 %). Both sides at their limits: 128 x 4096 x 4096 (M, N,
+// Cin) 8.3 us in 32-column tiles, 9.4 in 64 and 10.9 by pairs; 256 x 20480 x 4096 26.5 us by pairs
+// of 128, 29.1 by pairs of 256 and 39.0 split; 1 x 4096 x 10240 10.3 us split in 4, 13.3 unsplit.
+// clusters(bn, S): how many clusters of S CTAs the device holds at once.
+template <class Clusters>
+I8Plan plan_i8(int M, int N, int num_kblk, int num_sms, Clusters clusters) {
     // CONV_B200_I8 (tests): "pair,BN", or "split,BN,S"
     if (const char *f = env("CONV_B200_I8")) {
         int bn = 0, s = 0;
-        if (std::sscanf(f, "pair,%d", &bn) == 1 && (bn == 128 || bn == 256)) pl = I8Plan{true, bn, 1};
-        else if (std::sscanf(f, "split,%d,%d", &bn, &s) == 2 && (bn == 16 || bn == 32 || bn == 64 || bn == 128) &&
-                 (s == 1 || s == 2 || s == 4 || s == 8) && s <= (num_kblk + 1) / 2)
-            pl = I8Plan{false, bn, s};
+        if (std::sscanf(f, "pair,%d", &bn) == 1 && (bn == 128 || bn == 256)) return I8Plan{true, bn, 1};
+        if (std::sscanf(f, "split,%d,%d", &bn, &s) == 2 && (bn == 16 || bn == 32 || bn == 64 || bn == 128) &&
+            (s == 1 || s == 2 || s == 4 || s == 8) && s <= (num_kblk + 1) / 2)
+            return I8Plan{false, bn, s};
     }
-    return pl;
+    auto cdiv = [](long long a, long long b) { return (a + b - 1) / b; };
+    const float mbytes = (static_cast<float>(M) + N) * num_kblk * 128e-6f + 2e-6f * M * N;
+    const float l2 = 128 / 19.8e6f;   // us a row of 128 bytes through L2
+    I8Plan best{true, 256, 1};
+    float least = 3.4e38f;
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        const long long tiles = cdiv(M, 256) * cdiv(N, bn), pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+        const float rounds = static_cast<float>(cdiv(tiles, num_sms / 2));
+        const float kblk = fmaxf(bn == 256 ? 0.293f : 0.174f, l2 * pairs * (256 + bn));
+        const float t = 3.4f + rounds * (bn == 256 ? 2.3f : 1.5f) + hypotf(rounds * num_kblk * kblk, mbytes / 10.2f);
+        if (t < least) {
+            least = t;
+            best = I8Plan{true, bn, 1};
+        }
+    }
+    if (M > 512) return best;
+    for (int bn = 128; bn >= 16; bn /= 2) {
+        if (bn >= 2 * M && bn > 16) continue;   // half of the columns and more would be empty
+        const long long tiles = cdiv(M, bn) * cdiv(N, 128);
+        const float cols = static_cast<float>(bn < M ? bn : M);
+        for (int S = 1; S <= 8; S *= 2) {
+            const long long ctas = tiles * S;
+            // a split that does not run at once only adds to the work
+            if (S > 1 && (ctas > num_sms || 2 * S > num_kblk || tiles > clusters(bn, S))) break;
+            const int kb = i8_slot_kblks(bn, bn <= 32 && ctas > num_sms);
+            const float rounds = static_cast<float>(cdiv(ctas, num_sms));
+            const float share = static_cast<float>(cdiv(cdiv(num_kblk, kb), S) * kb);
+            const float own = bn == 128 ? 0.177f : bn == 64 ? 0.132f : bn == 32 ? 0.121f : 0.135f;
+            const float kblk = fmaxf(own, l2 * (ctas < num_sms ? ctas : num_sms) * (128 + bn));
+            const float t = 2.0f + rounds * (0.019f * cols + (S > 1 ? 0.62f + 0.013f * cols : 0.0f)) +
+                            hypotf(rounds * share * kblk, mbytes / 5.9f);
+            if (t < least) {
+                least = t;
+                best = I8Plan{false, bn, S};
+            }
+        }
+    }
+    return best;
+}
+
+template <class Cfg, typename OUT>
+int i8_split_clusters(DeviceState *d, unsigned bit, int S) {
+    auto kern = i8_split_kernel<Cfg, OUT>;
+    if (ensure_smem_attr(d, bit, kern, Cfg::SMEM)) return 0;
+    return cluster_fit(d, bit, kern, S, Cfg::SMEM, Cfg::THREADS);
 }
 
 template <typename OUT>
 int run_i8_product(const I8Operands &a, I8GemmParams p, cudaStream_t stream, DeviceState *d) {
+    constexpr unsigned bit = sizeof(OUT) == 4 ? 148 : 132;
+    // one CTA per SM has the whole shared memory for copies in flight; beyond that two share an SM
+    using Split16 = I8SplitCfg<16, 6, i8_slot_kblks(16, false)>;
+    using Split32 = I8SplitCfg<32, 5, i8_slot_kblks(32, false)>;
+    using Split64 = I8SplitCfg<64, 4, i8_slot_kblks(64, false)>;
+    using Split128 = I8SplitCfg<128, 5, i8_slot_kblks(128, false)>;
     p.num_kblk = (a.Cin + 127) / 128;
     p.vec = aligned(p.Y, 16) && (1LL * p.N * sizeof(OUT)) % 16 == 0;
-    const I8Plan pl = plan_i8(p.M, p.N, p.num_kblk, d->num_sms);
-    constexpr unsigned bit = sizeof(OUT) == 4 ? 148 : 132;
+    const I8Plan pl = plan_i8(p.M, p.N, p.num_kblk, d->num_sms, [&](int bn, int S) {
+        return bn == 16 ? i8_split_clusters<Split16, OUT>(d, bit + 2, S) : bn == 32 ? i8_split_clusters<Split32, OUT>(d, bit + 4, S)
+             : bn == 64 ? i8_split_clusters<Split64, OUT>(d, bit + 6, S) : i8_split_clusters<Split128, OUT>(d, bit + 7, S);
+    });
     if (pl.pair)
         return pl.bn == 256 ? launch_i8_pair<I8PairCfg<256, 5>, OUT>(a, p, stream, d, bit)
                             : launch_i8_pair<I8PairCfg<128, 7>, OUT>(a, p, stream, d, bit + 1);
-    // one CTA per SM has the whole shared memory for copies in flight; with more, two share an SM
-    const long long ctas = 1LL * ((p.N + 127) / 128) * ((p.M + pl.bn - 1) / pl.bn) * pl.split;
-    const bool deep = ctas <= d->num_sms;
+    const bool shared = 1LL * ((p.N + 127) / 128) * ((p.M + pl.bn - 1) / pl.bn) * pl.split > d->num_sms;
     switch (pl.bn) {
         case 16:
-            return deep ? launch_i8_split<I8SplitCfg<16, 6, 2>, OUT>(a, p, pl.split, stream, d, bit + 2)
-                        : launch_i8_split<I8SplitCfg<16, 5, 1>, OUT>(a, p, pl.split, stream, d, bit + 3);
+            return shared ? launch_i8_split<I8SplitCfg<16, 5, i8_slot_kblks(16, true)>, OUT>(a, p, pl.split, stream, d, bit + 3)
+                          : launch_i8_split<Split16, OUT>(a, p, pl.split, stream, d, bit + 2);
         case 32:
-            return deep ? launch_i8_split<I8SplitCfg<32, 5, 2>, OUT>(a, p, pl.split, stream, d, bit + 4)
-                        : launch_i8_split<I8SplitCfg<32, 4, 1>, OUT>(a, p, pl.split, stream, d, bit + 5);
-        case 64: return launch_i8_split<I8SplitCfg<64, 4, 2>, OUT>(a, p, pl.split, stream, d, bit + 6);
-        default: return launch_i8_split<I8SplitCfg<128, 5, 1>, OUT>(a, p, pl.split, stream, d, bit + 7);
+            return shared ? launch_i8_split<I8SplitCfg<32, 4, i8_slot_kblks(32, true)>, OUT>(a, p, pl.split, stream, d, bit + 5)
+                          : launch_i8_split<Split32, OUT>(a, p, pl.split, stream, d, bit + 4);
+        case 64: return launch_i8_split<Split64, OUT>(a, p, pl.split, stream, d, bit + 6);
+        default: return launch_i8_split<Split128, OUT>(a, p, pl.split, stream, d, bit + 7);
     }
 }
 
