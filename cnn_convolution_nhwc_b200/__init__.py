@@ -407,25 +407,49 @@ def dwpw_fwd(x, w_dw, b_dw, F, b_pw=None, y=None, stride=1, pad=0, dil=1, mode=D
 
 
 # ---- 8-bit operators ---------------------------------------------------------------------
-# Their single-token calls take a few microseconds on the GPU, so these wrappers keep to a few on
-# the host: one test per tensor on the good path (the messages come from the slow one), torch looked
-# up once, and the device switched only when it is not the current one.
-_BF16 = _F32 = _INT8 = _raw_stream = _current_device = None
+# A single-token call of these takes 2 to 5 us on the GPU, so the host's part counts. On the current
+# stream a call goes through _binding_i8 (csrc/binding_i8.cpp), which looks at the tensors in C++: 3
+# to 5 us with the outputs given. What it does not find in order, and a call with a stream named,
+# takes the checked way below, which says what is wrong.
+_BF16 = _F32 = _INT8 = _empty = _Tensor = _fast = None
+_ASK_SLOW = -1000
 
 
 def _i8_init():
-    global _BF16, _F32, _INT8, _raw_stream, _current_device
+    global _BF16, _F32, _INT8, _empty, _Tensor, _fast
+    import importlib.util
+
     import torch
-    _BF16, _F32, _INT8 = torch.bfloat16, torch.float32, torch.int8
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-        (lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _BF16, _F32, _INT8, _empty, _Tensor = torch.bfloat16, torch.float32, torch.int8, torch.empty, torch.Tensor
+    spec = importlib.util.spec_from_file_location("_binding_i8", _build.build_binding())
+    fast = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(fast)
+    fast.bind(*(ctypes.cast(f, _P).value for f in (lib.rmsnorm_i8_fwd, lib.quant_rows_i8_fwd, lib.quant_filter_i8_fwd,
+                                                   lib.dequant_rows_i8_fwd, lib.pointwise_i8_fwd)))
+    _fast = fast
+    return fast
+
+
+def _i8_is_matrix(t):
+    """Whether outputs can be shaped after t; otherwise the checked way says why not."""
+    if _fast is None:
+        _i8_init()
+    return isinstance(t, _Tensor) and t.ndim == 2 and t.is_cuda and t.numel() > 0
+
+
+def _i8_quick(rc, what):
+    """Whether the short path made the call; its error raised."""
+    if rc == CONV_OK:
+        return True
+    if rc != _ASK_SLOW:
+        _check(rc, what)
+    return False
 
 
 def _i8_matrix(x, name):
     """(conv_dtype, address) of a contiguous bfloat16 or float32 CUDA matrix."""
     import torch
-    if _BF16 is None:
+    if _fast is None:
         _i8_init()
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -437,52 +461,33 @@ def _i8_matrix(x, name):
 
 def _i8_ptr(t, dtype, shape, name):
     """The address of a contiguous CUDA tensor of the given type and shape."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _tensor(t, dtype, len(shape), name)
-    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    p = _tensor(t, dtype, len(shape), name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return p
 
 
 def _i8_rows(t, name):
     """(address, rows, columns, row pitch) of an int8 matrix whose rows start on 16-byte boundaries."""
-    try:
-        if t.dtype is _INT8 and t.is_cuda:
-            n, c = t.shape
-            pitch, step = t.stride()
-            if n < 2:
-                pitch = (c + 15) & ~15   # the stride of a dimension with one element means nothing
-            if (step == 1 or c < 2) and pitch >= c and not pitch & 15:
-                return t.data_ptr(), n, c, pitch
-    except (AttributeError, ValueError):
-        pass
     import torch
-    if _INT8 is None:
+    if _fast is None:
         _i8_init()
-        return _i8_rows(t, name)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not _INT8:
         raise TypeError(f"{name} must be torch.int8, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    raise ValueError(f"{name} must be an int8 matrix whose rows are contiguous and start on 16-byte boundaries "
-                     "(empty_rows_i8 makes one)")
-
-
-def _i8_call(fn, what, index, tensors, stream, *args):
-    """_call for the 8-bit entry points; `index`: the device of the first tensor."""
-    if stream is None and index == _current_device():
-        for t in tensors:
-            if t is not None and t.get_device() != index:
-                _device(*tensors)
-        rc = fn(*args, _raw_stream(index))
-        if rc != CONV_OK:
-            _check(rc, what)
-    else:
-        _call(fn, what, tensors, stream, *args)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got {t.dim()}")
+    n, c = t.shape
+    pitch, step = t.stride()
+    if n < 2:
+        pitch = (c + 15) // 16 * 16   # the stride of a dimension with one element means nothing
+    if (step != 1 and c > 1) or pitch < c or pitch % 16:
+        raise ValueError(f"{name} must be an int8 matrix whose rows are contiguous and start on 16-byte boundaries "
+                         "(empty_rows_i8 makes one)")
+    return t.data_ptr(), n, c, pitch
 
 
 def empty_rows_i8(rows, C, device="cuda"):
@@ -529,6 +534,14 @@ def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-
     a residual), then h * weight / sqrt(mean(h^2) + eps) as int8 q [M, C] and float32 scale [M].
     weight is float32 [C]. h may be x or residual (updated in place). Returns (q, scale, h); h is
     None without a residual."""
+    if stream is None:
+        oq, os, oh = q, scale, h
+        if (oq is None or os is None or (oh is None and residual is not None)) and _i8_is_matrix(x):
+            oq = empty_rows_i8(*x.shape, x.device) if oq is None else oq
+            os = _empty(x.shape[0], dtype=_F32, device=x.device) if os is None else os
+            oh = _empty(x.shape, dtype=x.dtype, device=x.device) if oh is None and residual is not None else oh
+        if _i8_quick((_fast or _i8_init()).rmsnorm(x, weight, residual, oh, oq, os, eps), "rmsnorm_i8_fwd"):
+            return oq, os, oh
     dt, px = _i8_matrix(x, "x")
     shape = x.shape
     M, C = shape
@@ -543,14 +556,22 @@ def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-
     elif h is not None:
         raise ValueError("h is x + residual: give the residual too")
     q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
-    _i8_call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", x.get_device(), (residual, weight, h, q, scale, x), stream,
-             px, pr, pw, ph, pq, ps, M, C, ldq, eps, dt)
+    _call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", (residual, weight, h, q, scale, x), stream,
+             px, pr, pw, ph, pq, ps, M, C, ldq, float(eps), dt)
     return q, scale, h
 
 
 def quant_rows_i8_fwd(x, glu=False, q=None, scale=None, stream=None):
     """8-bit rows of x [M, C] (bfloat16 or float32): int8 q [M, C] and float32 scale [M], one per row.
     With glu, x is [M, 2C] and the rows are silu(x[:, :C]) * x[:, C:]. Returns (q, scale)."""
+    if stream is None:
+        oq, os = q, scale
+        if (oq is None or os is None) and _i8_is_matrix(x):
+            C = x.shape[1]
+            oq = empty_rows_i8(x.shape[0], (C // 2 or 1) if glu else C, x.device) if oq is None else oq
+            os = _empty(x.shape[0], dtype=_F32, device=x.device) if os is None else os
+        if _i8_quick((_fast or _i8_init()).rows(x, oq, os, True if glu else False), "quant_rows_i8_fwd"):
+            return oq, os
     dt, px = _i8_matrix(x, "x")
     M, C = x.shape
     if glu:
@@ -558,7 +579,7 @@ def quant_rows_i8_fwd(x, glu=False, q=None, scale=None, stream=None):
             raise ValueError("glu needs x [M, 2C]")
         C //= 2
     q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
-    _i8_call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", x.get_device(), (q, scale, x), stream,
+    _call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", (q, scale, x), stream,
              px, pq, ps, M, C, ldq, 1 if glu else 0, dt)
     return q, scale
 
@@ -570,20 +591,33 @@ def quant_filter_i8_fwd(F, q=None, scale=None, stream=None):
         if tuple(F.shape[:2]) != (1, 1):
             raise ValueError("F must be a 1 x 1 filter")
         F = F[0, 0]
+    if stream is None:
+        oq, os = q, scale
+        if (oq is None or os is None) and _i8_is_matrix(F):
+            oq = empty_rows_i8(F.shape[1], F.shape[0], F.device) if oq is None else oq
+            os = _empty(F.shape[1], dtype=_F32, device=F.device) if os is None else os
+        if _i8_quick((_fast or _i8_init()).filter(F, oq, os), "quant_filter_i8_fwd"):
+            return oq, os
     dt, pf = _i8_matrix(F, "F")
     Cin, Cout = F.shape
     q, scale, pq, ldw, ps = _i8_out(q, scale, Cout, Cin, F.device)
-    _i8_call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", F.get_device(), (q, scale, F), stream,
+    _call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", (q, scale, F), stream,
              pf, pq, ps, Cin, Cout, ldw, dt)
     return q, scale
 
 
 def dequant_rows_i8_fwd(q, scale, y=None, dtype=None, stream=None):
     """Reads 8-bit rows back: y [M, C] = q * scale, in y's type (dtype, bfloat16 by default)."""
+    if stream is None and (y is None or dtype is None):
+        out = y
+        if y is None and _i8_is_matrix(q):
+            out = _empty(q.shape, dtype=dtype or _BF16, device=q.device)
+        if _i8_quick((_fast or _i8_init()).dequant(q, scale, out), "dequant_rows_i8_fwd"):
+            return out
     pq, M, C, ldq = _i8_rows(q, "q")
     ps = _i8_ptr(scale, _F32, (M,), "scale")
     y, dt, py = _i8_result(y, dtype, (M, C), q.device)
-    _i8_call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", q.get_device(), (scale, y, q), stream,
+    _call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", (scale, y, q), stream,
              pq, ps, py, M, C, ldq, dt)
     return y
 
@@ -591,6 +625,12 @@ def dequant_rows_i8_fwd(q, scale, y=None, dtype=None, stream=None):
 def pointwise_i8_fwd(q, q_scale, Wq, w_scale, bias=None, y=None, dtype=None, stream=None):
     """The product of 8-bit rows: y [M, Cout] = (q [M, Cin] @ Wq [Cout, Cin]^T) * q_scale [M] * w_scale [Cout]
     + bias [Cout], the sum exact in int32, in y's type (dtype, bfloat16 by default)."""
+    if stream is None and (y is None or dtype is None):
+        out = y
+        if y is None and _i8_is_matrix(q) and _i8_is_matrix(Wq):
+            out = _empty((q.shape[0], Wq.shape[0]), dtype=dtype or _BF16, device=q.device)
+        if _i8_quick((_fast or _i8_init()).pointwise(q, q_scale, Wq, w_scale, bias, out), "pointwise_i8_fwd"):
+            return out
     pq, M, Cin, ldq = _i8_rows(q, "q")
     pw, Cout, Cin2, ldw = _i8_rows(Wq, "Wq")
     if Cin2 != Cin:
@@ -598,7 +638,7 @@ def pointwise_i8_fwd(q, q_scale, Wq, w_scale, bias=None, y=None, dtype=None, str
     ps, pws = _i8_ptr(q_scale, _F32, (M,), "q_scale"), _i8_ptr(w_scale, _F32, (Cout,), "w_scale")
     pb = None if bias is None else _i8_ptr(bias, _F32, (Cout,), "bias")
     y, dt, py = _i8_result(y, dtype, (M, Cout), q.device)
-    _i8_call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", q.get_device(), (q_scale, Wq, w_scale, bias, y, q), stream,
+    _call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", (q_scale, Wq, w_scale, bias, y, q), stream,
              pq, ps, pw, pws, pb, py, M, Cin, Cout, ldq, ldw, dt)
     return y
 
@@ -627,8 +667,8 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
     if Y is None:
         Y = torch.empty((N, H, W, Cout), dtype=torch.bfloat16, device=X.device)
     py = _i8_ptr(Y, _BF16, (N, H, W, Cout), "Y")
-    _i8_call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", X.get_device(), (norm, Wq, w_scale, bias, Y, workspace, X), stream,
-             px, pn, eps, pw, pws, pb, py, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+    _call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", (norm, Wq, w_scale, bias, Y, workspace, X), stream,
+             px, pn, float(eps), pw, pws, pb, py, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
              N, H, W, Cin, Cout, ldw)
     return Y
 

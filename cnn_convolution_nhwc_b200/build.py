@@ -20,6 +20,9 @@ LIB = os.path.join(PKG, "libconv_b200.so")
 # copy checked against its tensor's extent (failures set a status bit and skip the access)
 LIB_DEBUG = os.path.join(PKG, "libconv_b200_debug.so")
 MAIN = os.path.join(PKG, "csrc", "capi.cu")
+# the short host path of the 8-bit operators: a Python extension over torch's C++ tensors
+BINDING = os.path.join(PKG, "_binding_i8.so")
+BINDING_SRC = os.path.join(PKG, "csrc", "binding_i8.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -30,7 +33,7 @@ NVCC_FLAGS = [
 
 
 def sources() -> list[str]:
-    return sorted(glob.glob(os.path.join(PKG, "csrc", "*")) + [os.path.join(ROOT, "include", "conv_b200.h")])
+    return sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu*")) + [os.path.join(ROOT, "include", "conv_b200.h")])
 
 
 def stale(lib: str = LIB) -> bool:
@@ -68,6 +71,35 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
         finally:
             fcntl.flock(lk, fcntl.LOCK_UN)
     return lib
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the Python extension of the 8-bit operators (csrc/binding_i8.cpp) against the torch
+    that runs, if it is missing or older than its source; returns its path."""
+    with open(os.path.join(PKG, ".build.lock"), "w") as lk:
+        fcntl.flock(lk, fcntl.LOCK_EX)
+        try:
+            if force or not os.path.exists(BINDING) or os.path.getmtime(BINDING_SRC) > os.path.getmtime(BINDING):
+                import sysconfig
+
+                import torch
+                base = os.path.dirname(torch.__file__)
+                tmp = BINDING + f".tmp{os.getpid()}"
+                cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                       f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                       "-I" + os.path.join(base, "include"),
+                       "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                       "-I" + sysconfig.get_paths()["include"],
+                       "-I" + os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include"),
+                       BINDING_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"),
+                       "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+                r = subprocess.run(cmd, capture_output=True, text=True)
+                if r.returncode != 0:
+                    raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+                os.replace(tmp, BINDING)
+        finally:
+            fcntl.flock(lk, fcntl.LOCK_UN)
+    return BINDING
 
 
 if __name__ == "__main__":

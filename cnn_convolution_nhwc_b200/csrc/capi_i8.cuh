@@ -238,7 +238,7 @@ I8Plan plan_i8(int M, int N, int num_kblk, int num_sms, Clusters clusters) {
         for (int S = 1; S <= 8; S *= 2) {
             const long long ctas = tiles * S;
             // a split that does not run at once only adds to the work
-            if (S > 1 && (ctas > num_sms || 2 * S > num_kblk || tiles > clusters(bn, S))) break;
+            if (S > 1 && (ctas > num_sms || 2 * S > num_kblk)) break;
             const int kb = i8_slot_kblks(bn, bn <= 32 && ctas > num_sms);
             const float rounds = static_cast<float>(cdiv(ctas, num_sms));
             const float share = static_cast<float>(cdiv(cdiv(num_kblk, kb), S) * kb);
@@ -246,7 +246,7 @@ I8Plan plan_i8(int M, int N, int num_kblk, int num_sms, Clusters clusters) {
             const float kblk = fmaxf(own, l2 * (ctas < num_sms ? ctas : num_sms) * (128 + bn));
             const float t = 2.0f + rounds * (0.019f * cols + (S > 1 ? 0.62f + 0.013f * cols : 0.0f)) +
                             hypotf(rounds * share * kblk, mbytes / 5.9f);
-            if (t < least) {
+            if (t < least && (S == 1 || tiles <= clusters(bn, S))) {
                 least = t;
                 best = I8Plan{false, bn, S};
             }

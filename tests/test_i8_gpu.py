@@ -409,3 +409,59 @@ def test_bounds_checked_build(cb, tmp_path):
     got = np.load(f)
     for k, v in run_all(cb).items():
         assert np.array_equal(v, got[k], equal_nan=True), k
+
+
+def test_short_and_checked_calls_agree(cb):
+    # every output given on the current stream: the C++ path; a stream named: the checked one
+    g = _gen(21)
+    s = torch.cuda.current_stream()
+    for M, C, N in ((1, 1024, 256), (5, 333, 70)):
+        x, r = _normal(g, M, C, dtype=torch.bfloat16), _normal(g, M, C, dtype=torch.bfloat16)
+        w, F, x2 = 1 + 0.1 * _normal(g, C), _normal(g, C, N), _normal(g, M, 2 * C)
+
+        def out(rows, cols):
+            return dict(q=cb.empty_rows_i8(rows, cols), scale=torch.empty(rows, device="cuda"))
+        a = cb.rmsnorm_i8_fwd(x, w, r, h=torch.empty_like(x), **out(M, C))
+        b = cb.rmsnorm_i8_fwd(x, w, r, stream=s)
+        c = cb.quant_rows_i8_fwd(x2, glu=True, **out(M, C)) + cb.quant_filter_i8_fwd(F, **out(N, C))
+        d = cb.quant_rows_i8_fwd(x2, glu=True, stream=s) + cb.quant_filter_i8_fwd(F, stream=s)
+        for t, u in zip(a + c, b + d):
+            assert torch.equal(t, u)
+        y = torch.empty(M, N, device="cuda")
+        assert torch.equal(cb.pointwise_i8_fwd(a[0], a[1], c[2], c[3], y=y), cb.pointwise_i8_fwd(a[0], a[1], c[2], c[3], dtype=torch.float32))
+        y = torch.empty(M, C, device="cuda")
+        assert torch.equal(cb.dequant_rows_i8_fwd(a[0], a[1], y=y), cb.dequant_rows_i8_fwd(a[0], a[1], dtype=torch.float32))
+    assert cb._fast.pointwise(a[0], a[1], c[2], c[3], None, torch.empty(M, N, device="cuda")) == cb.CONV_OK
+
+
+def test_binding_refuses_with_the_outputs_given(cb):
+    # what the short path leaves alone reaches the checked one, which names the argument
+    x = torch.zeros(4, 32, device="cuda", dtype=torch.bfloat16)
+    q, scale, w = cb.empty_rows_i8(4, 32), torch.empty(4, device="cuda"), torch.ones(32, device="cuda")
+    y = torch.empty(4, 4, device="cuda")
+    with pytest.raises(ValueError, match="scale must have shape"):
+        cb.quant_rows_i8_fwd(x, q=q, scale=scale[:3])
+    with pytest.raises(ValueError, match="q must have shape"):
+        cb.quant_rows_i8_fwd(x, q=q[:3], scale=scale)
+    with pytest.raises(ValueError, match="contiguous"):
+        cb.quant_rows_i8_fwd(x.t(), q=q, scale=scale)
+    with pytest.raises(TypeError, match="x must be"):
+        cb.quant_rows_i8_fwd(x.half(), q=q, scale=scale)
+    with pytest.raises(TypeError, match="weight must be"):
+        cb.rmsnorm_i8_fwd(x, w.half(), q=q, scale=scale)
+    with pytest.raises(ValueError, match="residual too"):
+        cb.rmsnorm_i8_fwd(x, w, h=x, q=q, scale=scale)
+    with pytest.raises(ValueError, match="16-byte"):
+        cb.pointwise_i8_fwd(torch.zeros(4, 40, dtype=torch.int8, device="cuda")[:, :32], scale,
+                            torch.zeros(4, 33, dtype=torch.int8, device="cuda")[:, :32], scale, y=y)
+    with pytest.raises(ValueError, match="columns"):
+        cb.pointwise_i8_fwd(q, scale, cb.empty_rows_i8(4, 48), scale, y=y)
+    with pytest.raises(ValueError, match="bias must have shape"):
+        cb.pointwise_i8_fwd(q, scale, q, scale, bias=w, y=y)
+    with pytest.raises(ValueError, match="CUDA"):
+        cb.dequant_rows_i8_fwd(q, scale, y=torch.empty(4, 32))
+    memory = torch.zeros(4 * 32, device="cuda")   # the library's own refusals: y on q's bytes, eps
+    with pytest.raises(cb.ConvError):
+        cb.dequant_rows_i8_fwd(memory.view(torch.int8)[:128].view(4, 32), scale, y=memory.view(4, 32))
+    with pytest.raises(cb.ConvError):
+        cb.rmsnorm_i8_fwd(x, w, eps=0.0, q=q, scale=scale)
