@@ -21,31 +21,34 @@ int check_i8_rows(const void *q, int C, int ld) {
 }
 
 // ---- rows ------------------------------------------------------------------------------
-template <typename T, int MODE, int NV, bool VEC, int TPR, bool STREAM>
+template <typename T, int MODE, int NV, bool VEC, int TPR, int RW, bool STREAM>
 int launch_i8_rows(const I8RowsParams &p, int threads, cudaStream_t stream, DeviceState *d) {
-    const long long per = TPR == 32 ? threads / 32 : 1, blocks = (p.M + per - 1) / per;
+    const long long per = TPR == 32 ? threads / 32 * RW : 1, blocks = (p.M + per - 1) / per;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.stream = stream;
-    return launched(launch_k(cfg, i8_rows_kernel<T, MODE, NV, VEC, TPR, STREAM>, p, d->status), "i8_rows_kernel");
+    return launched(launch_k(cfg, i8_rows_kernel<T, MODE, NV, VEC, TPR, RW, STREAM>, p, d->status), "i8_rows_kernel");
 }
 
 template <typename T, int MODE>
 int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
-    // A warp holds rows up to 1024 values, a block of up to 512 threads rows up to 16384.
+    // A warp holds rows up to 1024 values (two rows of up to 512: 25088 x 256 took 6.9 us with one,
+    // 4.9 with two, 5.0 with four; 48000 x 512 15.6, 14.5 and 17.0), a block of up to 512
+    // threads rows up to 16384.
     const int C = p.C;
     if (C % 8 == 0 && aligned(p.x, 16) && aligned(p.residual, 16) && aligned(p.h, 16) && aligned(p.weight, 16)) {
-        if (C <= 512) return launch_i8_rows<T, MODE, 2, true, 32, false>(p, 128, stream, d);
-        if (C <= 1024) return launch_i8_rows<T, MODE, 4, true, 32, false>(p, 128, stream, d);
-        if (C <= 16384) return launch_i8_rows<T, MODE, 4, true, 0, false>(p, (C + 1023) / 1024 * 32, stream, d);
-        return launch_i8_rows<T, MODE, 4, true, 0, true>(p, 512, stream, d);
+        if (C <= 256) return launch_i8_rows<T, MODE, 1, true, 32, 2, false>(p, 128, stream, d);
+        if (C <= 512) return launch_i8_rows<T, MODE, 2, true, 32, 2, false>(p, 128, stream, d);
+        if (C <= 1024) return launch_i8_rows<T, MODE, 4, true, 32, 1, false>(p, 128, stream, d);
+        if (C <= 16384) return launch_i8_rows<T, MODE, 4, true, 0, 1, false>(p, (C + 1023) / 1024 * 32, stream, d);
+        return launch_i8_rows<T, MODE, 4, true, 0, 1, true>(p, 512, stream, d);
     }
-    if (C <= 512) return launch_i8_rows<T, MODE, 2, false, 32, false>(p, 128, stream, d);
-    if (C <= 2048) return launch_i8_rows<T, MODE, 2, false, 128, false>(p, 128, stream, d);
-    if (C <= 4096) return launch_i8_rows<T, MODE, 2, false, 256, false>(p, 256, stream, d);
-    if (C <= 8192) return launch_i8_rows<T, MODE, 2, false, 512, false>(p, 512, stream, d);
-    return launch_i8_rows<T, MODE, 2, false, 512, true>(p, 512, stream, d);
+    if (C <= 512) return launch_i8_rows<T, MODE, 2, false, 32, 1, false>(p, 128, stream, d);
+    if (C <= 2048) return launch_i8_rows<T, MODE, 2, false, 128, 1, false>(p, 128, stream, d);
+    if (C <= 4096) return launch_i8_rows<T, MODE, 2, false, 256, 1, false>(p, 256, stream, d);
+    if (C <= 8192) return launch_i8_rows<T, MODE, 2, false, 512, 1, false>(p, 512, stream, d);
+    return launch_i8_rows<T, MODE, 2, false, 512, 1, true>(p, 512, stream, d);
 }
 
 template <int MODE>
@@ -328,7 +331,9 @@ int launch_pointwise_i8(const int8_t *q, const float *q_scale, const int8_t *Wq,
 
 extern "C" {
 
-int conv_i8_row_pitch(int C) { return C < 1 || C > kInt32Max - 15 ? 0 : (C + 15) / 16 * 16; }
+// Rows on 32-byte sectors: a tensor copy of rows that start inside one takes up to twice as long (301
+// x 4999 x 5003: 22.9 us with a pitch of 5008, 15.0 with 5024, 14.0 with 5120).
+int conv_i8_row_pitch(int C) { return C < 1 || C > kInt32Max - 31 ? 0 : (C + 31) / 32 * 32; }
 
 int rmsnorm_i8_fwd(const void *x, const void *residual, const float *weight, void *h, int8_t *q, float *scale, int M,
                    int C, int ldq, float eps, int dtype, cudaStream_t stream) {
@@ -448,15 +453,17 @@ int conv2d_nhwc_fwd_i8(const void *X, const float *norm, float eps, const int8_t
     if (!X || !Wq || !w_scale || !Y || !workspace) return CONV_ERR_INVALID_ARG;
     if (N < 1 || H < 1 || W < 1 || Cin < 1 || Cout < 1 || ldw < Cin) return CONV_ERR_INVALID_ARG;
     if (norm && (!(eps >= 0x1p-126f) || !(eps <= 3.402823466e+38f))) return CONV_ERR_INVALID_ARG;
-    const size_t need = conv2d_nhwc_i8_workspace(N, H, W, Cin);
-    if (need == 0) return CONV_ERR_UNSUPPORTED;
-    if (workspace_bytes < need) return CONV_ERR_INVALID_ARG;
+    const size_t full = conv2d_nhwc_i8_workspace(N, H, W, Cin);
+    if (full == 0) return CONV_ERR_UNSUPPORTED;
+    const int ld16 = (Cin + 15) / 16 * 16;
+    const size_t least = 1ull * N * H * W * (ld16 + 4);
+    if (workspace_bytes < least) return CONV_ERR_INVALID_ARG;
     if (!aligned(workspace, 16) || !aligned(X, 2) || !aligned(norm, 4)) return CONV_ERR_MISALIGNED;
-    const int M = N * H * W, ldq = conv_i8_row_pitch(Cin);
+    const int M = N * H * W, ldq = workspace_bytes >= full ? conv_i8_row_pitch(Cin) : ld16;
     int8_t *q = static_cast<int8_t *>(workspace);
     float *q_scale = reinterpret_cast<float *>(q + 1LL * M * ldq);
     if (int rc = check_pointwise_i8(q, q_scale, Wq, w_scale, bias, Y, M, Cin, Cout, ldq, ldw, CONV_BF16)) return rc;
-    const long long nx = 2LL * M * Cin, ny = 2LL * M * Cout, nws = static_cast<long long>(need);
+    const long long nx = 2LL * M * Cin, ny = 2LL * M * Cout, nws = 1LL * M * (ldq + 4);
     if (overlaps(Y, ny, X, nx) || (norm && overlaps(Y, ny, norm, 4LL * Cin)) || overlaps(workspace, nws, X, nx) ||
         overlaps(workspace, nws, Wq, i8_extent(Cout, Cin, ldw)) || overlaps(workspace, nws, w_scale, 4LL * Cout) ||
         (bias && overlaps(workspace, nws, bias, 4LL * Cout)) || (norm && overlaps(workspace, nws, norm, 4LL * Cin)))

@@ -248,101 +248,117 @@ __device__ __forceinline__ uint2 i8_quant8(const uint64_t (&t)[4], const I8RowSc
     return make_uint2(i8_bytes(b[0], b[1], b[2], b[3]), i8_bytes(b[4], b[5], b[6], b[7]));
 }
 
-// One row per group of threads: a warp (TPR = 32) or a block. A thread holds NV groups of eight
-// values in registers, so a row of up to 8 * NV values a thread is read once; a longer row (STREAM)
-// is walked in pieces of that size twice, the second time from h (or x), which the first pass
-// left in L2. All of a thread's loads are issued before the first is used: with four groups a
-// thread that keeps 100 KB and more of loads in flight per SM.
+// One row per group of threads: a block, or a warp (TPR = 32), which takes RW rows at once. A thread
+// holds NV groups of eight values of a row in registers, so a row of up to 8 * NV values a thread is
+// read once; a longer row (STREAM) is walked in pieces of that size twice, the second time from h
+// (or x), which the first pass left in L2. All of a thread's loads are issued before the first is
+// used: with four groups a thread (of one row or several) that keeps 100 KB and more of loads in
+// flight per SM.
 // VEC: tensors on 16 bytes and C a multiple of 8; a thread's eight values are neighbours and move in
 // 16-byte accesses; a block has the threads that the row needs (TPR = 0). Otherwise any C and any
 // pointers: neighbouring lanes hold neighbouring values, an element an access, and a thread's values
 // are TPR apart, a constant, so that its accesses need no address arithmetic.
-template <typename T, int MODE, int NV, bool VEC, int TPR, bool STREAM>
+template <typename T, int MODE, int NV, bool VEC, int TPR, int RW, bool STREAM>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : 512)
 i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
     grid_dependents_launch();   // programmatic dependent launch (see ptx.cuh)
     grid_dependency_wait();
     constexpr bool NORM = MODE == kI8Norm || MODE == kI8NormResidual;
     constexpr bool GROUP_WARP = TPR == 32;
+    static_assert(RW == 1 || (GROUP_WARP && !STREAM), "several rows: a warp's, in registers");
     constexpr bool BF16 = MODE == kI8Plain && sizeof(T) == 2;   // the rounded values are bf16 values
     __shared__ float s_sum[16];
     __shared__ uint32_t s_max[16];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tpr = TPR != 0 ? TPR : static_cast<int>(blockDim.x);
     const int tid = GROUP_WARP ? lane : static_cast<int>(threadIdx.x);
-    const long long row = GROUP_WARP ? 1LL * blockIdx.x * (blockDim.x >> 5) + warp : static_cast<long long>(blockIdx.x);
-    if (row >= p.M) return;   // whole warps only, and no block barrier follows for GROUP_WARP
+    const long long row0 = GROUP_WARP ? (1LL * blockIdx.x * (blockDim.x >> 5) + warp) * RW : static_cast<long long>(blockIdx.x);
+    if (row0 >= p.M) return;   // whole warps only, and no block barrier follows for GROUP_WARP
     const int C = p.C;
-    const long long xrow = row * C * (MODE == kI8Glu ? 2 : 1), hrow = row * C;
     const long long n_elems = p.M * C, x_elems = n_elems * (MODE == kI8Glu ? 2 : 1);   // bounds checks (debug build)
-    const T *x = static_cast<const T *>(p.x) + xrow;
-    const T *second = MODE == kI8Glu ? x + C : static_cast<const T *>(p.residual) + hrow;   // up, or the residual
-    T *h = static_cast<T *>(p.h) + hrow;
-    int8_t *q = p.q + row * p.ldq;
+
+    const T *x = static_cast<const T *>(p.x);
+    const T *second = MODE == kI8Glu ? x : static_cast<const T *>(p.residual);   // up, or the residual
+    T *h = static_cast<T *>(p.h);
+    // the elements and bytes at which row r of the group's starts
+    struct Row {
+        long long x, second, h, q;
+        bool live;
+    };
+    auto of = [&](int r) {
+        const long long row = row0 + r;
+        const long long e = row * C * (MODE == kI8Glu ? 2 : 1);
+        return Row{e, MODE == kI8Glu ? e + C : e, row * C, row * p.ldq, RW == 1 || row < p.M};
+    };
 
     // column of value i of group k in the piece that starts at c0
     auto at = [&](int c0, int k, int i) { return VEC ? c0 + (k * tpr + tid) * 8 + i : c0 + (k * 8 + i) * tpr + tid; };
 
-    // Reads a piece: the values t that are rounded; the norms add the squares of h to `sum`.
-    // first: the row's first pass, which writes h.
-    auto load = [&](int c0, bool first, uint64_t (&t)[NV][4], uint64_t &sum) {
+    // Reads a piece of the warp's or block's rows: the values t that are rounded; the norms add the
+    // squares of h to `sum`. first: the rows' first pass, which writes h.
+    auto load = [&](int c0, bool first, uint64_t (&t)[RW][NV][4], uint64_t (&sum)[RW]) {
         const bool from_h = MODE == kI8NormResidual && !first;
         const bool two = MODE == kI8Glu || (MODE == kI8NormResidual && first);
-        const T *src = from_h ? h : x;
         if constexpr (VEC) {
-            I8Raw<T> a[NV], b[NV];
+            I8Raw<T> a[RW][NV], b[RW][NV];
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = at(c0, k, 0);
-                const bool in = c < C && in_bounds(xrow + c, 8, x_elems, kSiteI8RowsX, status);
-                a[k] = in ? i8_raw_load(src + c) : i8_raw_zero<T>();
-                if (two) b[k] = in ? i8_raw_load(second + c) : i8_raw_zero<T>();
-            }
+            for (int r = 0; r < RW; ++r)
 #pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = at(c0, k, 0);
-                i8_unpack(a[k], t[k]);
+                for (int k = 0; k < NV; ++k) {
+                    const int c = at(c0, k, 0);
+                    const Row w = of(r);
+                    const bool in = c < C && w.live && in_bounds(w.x + c, 8, x_elems, kSiteI8RowsX, status);
+                    a[r][k] = in ? i8_raw_load((from_h ? h : x) + w.x + c) : i8_raw_zero<T>();
+                    if (two) b[r][k] = in ? i8_raw_load(second + w.second + c) : i8_raw_zero<T>();
+                }
+            uint64_t w[4];
+#pragma unroll
+            for (int kr = 0; kr < NV * RW; ++kr) {
+                const int k = kr / RW, r = kr % RW, c = at(c0, k, 0);
+                const Row row = of(r);
+                i8_unpack(a[r][k], t[r][k]);
                 uint64_t u[4];
                 if constexpr (MODE == kI8Glu) {
-                    i8_unpack(b[k], u);
+                    i8_unpack(b[r][k], u);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         float g0, g1, u0, u1;
-                        f2_split(t[k][i], g0, g1);
+                        f2_split(t[r][k][i], g0, g1);
                         f2_split(u[i], u0, u1);
-                        t[k][i] = f2_pack(i8_glu(g0, u0), i8_glu(g1, u1));
+                        t[r][k][i] = f2_pack(i8_glu(g0, u0), i8_glu(g1, u1));
                     }
                 }
                 if constexpr (MODE == kI8NormResidual) {
                     if (first) {
-                        i8_unpack(b[k], u);
+                        i8_unpack(b[r][k], u);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) t[k][i] = f2_add(t[k][i], u[i]);
-                        i8_pack(t[k], a[k]);
-                        i8_unpack(a[k], t[k]);
-                        if (c < C) i8_raw_store(h + c, a[k]);
+                        for (int i = 0; i < 4; ++i) t[r][k][i] = f2_add(t[r][k][i], u[i]);
+                        i8_pack(t[r][k], a[r][k]);
+                        i8_unpack(a[r][k], t[r][k]);
+                        if (c < C && row.live) i8_raw_store(h + row.x + c, a[r][k]);
                     }
                 }
                 if constexpr (NORM) {
-                    uint64_t w[4];
-                    i8_unpack(i8_raw_load(p.weight + (c < C ? c : 0)), w);
+                    if (r == 0) i8_unpack(i8_raw_load(p.weight + (c < C ? c : 0)), w);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        sum = f2_fma(t[k][i], t[k][i], sum);
-                        t[k][i] = f2_mul(t[k][i], w[i]);
+                        sum[r] = f2_fma(t[r][k][i], t[r][k][i], sum[r]);
+                        t[r][k][i] = f2_mul(t[r][k][i], w[i]);
                     }
                 }
             }
         } else {
+            static_assert(VEC || RW == 1, "element accesses: one row");
+            const Row row = of(0);
             float a[NV][8], b[NV][8], w[NV][8];
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int c = at(c0, k, i);
-                    const bool in = c < C && in_bounds(xrow + c, 1, x_elems, kSiteI8RowsX, status);
-                    a[k][i] = in ? i8_to_float(src[c]) : 0.0f;
-                    if (two) b[k][i] = in ? i8_to_float(second[c]) : 0.0f;
+                    const bool in = c < C && in_bounds(row.x + c, 1, x_elems, kSiteI8RowsX, status);
+                    a[k][i] = in ? i8_to_float((from_h ? h : x)[row.x + c]) : 0.0f;
+                    if (two) b[k][i] = in ? i8_to_float(second[row.second + c]) : 0.0f;
                     if (NORM) w[k][i] = c < C ? p.weight[c] : 0.0f;
                 }
 #pragma unroll
@@ -354,96 +370,111 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
                     if constexpr (MODE == kI8NormResidual) {
                         if (first) {
                             a[k][i] = i8_round_to(a[k][i] + b[k][i], T());
-                            if (c < C) h[c] = static_cast<T>(a[k][i]);
+                            if (c < C) h[row.x + c] = static_cast<T>(a[k][i]);
                         }
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    t[k][i] = f2_pack(a[k][2 * i], a[k][2 * i + 1]);
+                    t[0][k][i] = f2_pack(a[k][2 * i], a[k][2 * i + 1]);
                     if constexpr (NORM) {
-                        sum = f2_fma(t[k][i], t[k][i], sum);
-                        t[k][i] = f2_mul(t[k][i], f2_pack(w[k][2 * i], w[k][2 * i + 1]));
+                        sum[0] = f2_fma(t[0][k][i], t[0][k][i], sum[0]);
+                        t[0][k][i] = f2_mul(t[0][k][i], f2_pack(w[k][2 * i], w[k][2 * i + 1]));
                     }
                 }
             }
         }
     };
-    auto store = [&](int c0, int k, uint2 b) {
+    auto store = [&](int c0, int r, int k, uint2 b) {
+        const Row row = of(r);
+        int8_t *q = p.q + row.q;
         if constexpr (VEC) {
             const int c = at(c0, k, 0);
-            if (c < C && in_bounds(hrow + c, 8, n_elems, kSiteI8RowsQ, status)) *reinterpret_cast<uint2 *>(q + c) = b;
+            if (c < C && row.live && in_bounds(row.h + c, 8, n_elems, kSiteI8RowsQ, status)) *reinterpret_cast<uint2 *>(q + c) = b;
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = at(c0, k, i);
-                if (c < C && in_bounds(hrow + c, 1, n_elems, kSiteI8RowsQ, status))
+                if (c < C && in_bounds(row.h + c, 1, n_elems, kSiteI8RowsQ, status))
                     q[c] = static_cast<int8_t>((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
             }
         }
     };
 
-    uint64_t t[NV][4];
-    uint64_t sum2 = 0;      // of the squares, even and odd values apart
-    float top = 0.0f;       // the largest magnitude, or NaN
+    uint64_t t[RW][NV][4];
+    uint64_t sum2[RW];      // of the squares, even and odd values apart
+    float top[RW];          // the largest magnitude, or NaN
+#pragma unroll
+    for (int r = 0; r < RW; ++r) {
+        sum2[r] = 0;
+        top[r] = 0.0f;
+    }
     const int piece = tpr * 8 * NV;
     for (int c0 = 0; c0 < (STREAM ? C : 1); c0 += piece) {
         load(c0, true, t, sum2);
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
+        for (int r = 0; r < RW; ++r)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float lo, hi;
-                f2_split(t[k][i], lo, hi);
-                top = max3_abs(top, lo, hi);
-            }
+            for (int k = 0; k < NV; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float lo, hi;
+                    f2_split(t[r][k][i], lo, hi);
+                    top[r] = max3_abs(top[r], lo, hi);
+                }
         if (C - c0 <= piece) break;   // c0 + piece may pass the int range
     }
-    uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);   // magnitudes are ordered as their bits
-    float sum = 0.0f;
-    if constexpr (NORM) {
-        float lo, hi;
-        f2_split(sum2, lo, hi);
-        sum = lo + hi;
+    I8RowScale s[RW];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
-    if constexpr (!GROUP_WARP) {
-        if (lane == 0) {
-            s_max[warp] = amax;
-            s_sum[warp] = sum;
-        }
-        __syncthreads();
-        const int warps = tpr >> 5;
-        amax = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
+    for (int r = 0; r < RW; ++r) {
+        // magnitudes are ordered as their bits, NaN above infinity
+        uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top[r]) & 0x7fffffffu);
+        float sum = 0.0f;
         if constexpr (NORM) {
-            sum = lane < warps ? s_sum[lane] : 0.0f;
+            float lo, hi;
+            f2_split(sum2[r], lo, hi);
+            sum = lo + hi;
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            sum = __shfl_sync(0xffffffffu, sum, 0);
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-    }
-    const bool finite = amax < 0x7f800000u && (!NORM || sum < __uint_as_float(0x7f800000u));
-    const I8RowScale s = i8_row_scale(amax, finite);
-    if (tid == 0) {
-        const float A = __uint_as_float(amax);
-        float sc = NORM ? A * (1.0f / sqrtf(sum / static_cast<float>(C) + p.eps)) / 127.0f : A / 127.0f;
-        if (amax == 0u) sc = 0.0f;
-        if (!finite) sc = __uint_as_float(0x7fc00000u);
-        if (in_bounds(row, 1, p.M, kSiteI8RowsScale, status)) p.scale[row] = sc;
+        if constexpr (!GROUP_WARP) {
+            if (lane == 0) {
+                s_max[warp] = amax;
+                s_sum[warp] = sum;
+            }
+            __syncthreads();
+            const int warps = tpr >> 5;
+            amax = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
+            if constexpr (NORM) {
+                sum = lane < warps ? s_sum[lane] : 0.0f;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                sum = __shfl_sync(0xffffffffu, sum, 0);
+            }
+        }
+        const bool finite = amax < 0x7f800000u && (!NORM || sum < __uint_as_float(0x7f800000u));
+        s[r] = i8_row_scale(amax, finite);
+        if (tid == 0 && row0 + r < p.M) {
+            const float A = __uint_as_float(amax);
+            float sc = NORM ? A * (1.0f / sqrtf(sum / static_cast<float>(C) + p.eps)) / 127.0f : A / 127.0f;
+            if (amax == 0u) sc = 0.0f;
+            if (!finite) sc = __uint_as_float(0x7fc00000u);
+            if (in_bounds(row0 + r, 1, p.M, kSiteI8RowsScale, status)) p.scale[row0 + r] = sc;
+        }
     }
     for (int c0 = 0; c0 < (STREAM ? C : 1); c0 += piece) {
         if constexpr (STREAM) {
-            uint64_t unused = 0;
+            uint64_t unused[RW] = {};
             load(c0, false, t, unused);
         }
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            if (s.up != 1.0f) {
+        for (int rk = 0; rk < RW * NV; ++rk) {
+            const int r = rk / NV, k = rk % NV;
+            if (s[r].up != 1.0f) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) t[k][i] = f2_mul(t[k][i], f2_pack(s.up, s.up));
+                for (int i = 0; i < 4; ++i) t[r][k][i] = f2_mul(t[r][k][i], f2_pack(s[r].up, s[r].up));
             }
-            store(c0, k, s.dead ? make_uint2(0u, 0u) : i8_quant8<BF16>(t[k], s));
+            store(c0, r, k, s[r].dead ? make_uint2(0u, 0u) : i8_quant8<BF16>(t[r][k], s[r]));
         }
         if (C - c0 <= piece) break;
     }

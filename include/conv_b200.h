@@ -260,9 +260,10 @@ int dwpw_fwd(const float *x, const float *w_dw, const float *b_dw, const void *F
  * cores' rate.
  *
  * 8-bit rows: a matrix of M rows of C bytes is int8_t q[M][ld] with ld >= C bytes from row to
- * row, ld a multiple of 16 and q 16-byte aligned (conv_i8_row_pitch(C) is the smallest such ld; 0
- * for a C out of range). The bytes between C and ld are neither read nor written. A row's values
- * are q[c] * scale.
+ * row, ld a multiple of 16 and q 16-byte aligned. conv_i8_row_pitch(C) is the ld to take, C rounded
+ * up to 32 (0 for a C out of range); other multiples of 16 work, and those that are not multiples of
+ * 32 make the product's copies slower. The bytes between C and ld are neither read nor written. A
+ * row's values are q[c] * scale.
  *
  * Rounding of a row v with A = max |v[c]| > 0: q[c] is 127 v[c] / A rounded to the nearest integer,
  * ties to even (the real quotient of the float32 values, whatever the shape), scale = A / 127. A row
@@ -339,9 +340,10 @@ int pointwise_i8_fwd(const int8_t *q, const float *q_scale, const int8_t *Wq, co
  * into the workspace, then pointwise_i8_fwd, with exactly their results.
  *   X : bfloat16 [N][H][W][Cin];  Y : bfloat16 [N][H][W][Cout]
  *   Wq [Cout][ldw], w_scale, bias : as pointwise_i8_fwd
- *   workspace : DEVICE memory, at least conv2d_nhwc_i8_workspace() bytes, 16-byte aligned, not
- *               overlapping the tensors; overwritten. Calls that may run at the same time
- *               (different streams) need one each.
+ *   workspace : DEVICE memory, 16-byte aligned, not overlapping the tensors; overwritten.
+ *               conv2d_nhwc_i8_workspace() bytes hold the rows at conv_i8_row_pitch(Cin);
+ *               N*H*W * (Cin rounded up to 16, plus 4) bytes are enough. Calls that may run at
+ *               the same time (different streams) need one each.
  * eps is ignored without norm. Requirements: N, H, W, Cin, Cout >= 1; N*H*W below 2^31 and
  * Cin <= 131071 (else CONV_ERR_UNSUPPORTED).
  */

@@ -19,9 +19,9 @@ def off(p, n):
 
 
 def test_row_pitch():
-    assert [cb.lib.conv_i8_row_pitch(c) for c in (1, 15, 16, 17, 4096, 4097)] == [16, 16, 16, 32, 4096, 4112]
+    assert [cb.lib.conv_i8_row_pitch(c) for c in (1, 15, 16, 17, 33, 4096, 4097)] == [32, 32, 32, 32, 64, 4096, 4128]
     assert cb.lib.conv_i8_row_pitch(0) == 0 and cb.lib.conv_i8_row_pitch(-3) == 0
-    assert cb.lib.conv_i8_row_pitch(2 ** 31 - 16) == 2 ** 31 - 16 and cb.lib.conv_i8_row_pitch(2 ** 31 - 1) == 0
+    assert cb.lib.conv_i8_row_pitch(2 ** 31 - 32) == 2 ** 31 - 32 and cb.lib.conv_i8_row_pitch(2 ** 31 - 1) == 0
 
 
 @pytest.mark.parametrize("args,code", [
@@ -142,7 +142,7 @@ def test_layer_rejects(args, code):
 
 def test_layer_workspace():
     assert cb.lib.conv2d_nhwc_i8_workspace(2, 3, 5, 20) == 30 * (32 + 4)
-    assert cb.lib.conv2d_nhwc_i8_workspace(1, 1, 1, 16) == 20
+    assert cb.lib.conv2d_nhwc_i8_workspace(1, 1, 1, 16) == 36
     assert cb.lib.conv2d_nhwc_i8_workspace(0, 3, 5, 20) == 0
     assert cb.lib.conv2d_nhwc_i8_workspace(1, 1, 1, 131072) == 0
     assert cb.lib.conv2d_nhwc_i8_workspace(65536, 65536, 65536, 16) == 0

@@ -32,8 +32,9 @@ def _normal(g, *shape, dtype=torch.float32):
 
 def _bytes(g, rows, C, cb, lo=-127):
     """Random 8-bit rows whose gap between C and the pitch holds garbage."""
-    q = cb.empty_rows_i8(rows, C)
-    q._base.fill_(77) if q._base is not None else None
+    # a pitch of 16 bytes more than a multiple of 32 for some shapes
+    pitch = (C + 15) // 16 * 16
+    q = torch.full((rows, pitch), 77, dtype=torch.int8, device="cuda")[:, :C]
     q.copy_(torch.randint(lo, 128, (rows, C), generator=g, device="cuda"))
     return q
 
@@ -225,6 +226,9 @@ def test_layer_is_its_parts(cb, shape):
     x = X.reshape(-1, Cin)
     for n in (None, norm):
         Y = cb.conv2d_nhwc_fwd_i8(X, wq, ws, bias, norm=n, eps=1e-5)
+        # a workspace for the pitch of 32 bytes, and the smallest one, at 16
+        small = torch.empty(N * H * W * ((Cin + 15) // 16 * 16 + 4), dtype=torch.uint8, device="cuda")
+        assert torch.equal(Y, cb.conv2d_nhwc_fwd_i8(X, wq, ws, bias, norm=n, eps=1e-5, workspace=small))
         q, s = cb.quant_rows_i8_fwd(x) if n is None else cb.rmsnorm_i8_fwd(x, n, eps=1e-5)[:2]
         assert torch.equal(Y.reshape(-1, Cout), cb.pointwise_i8_fwd(q, s, wq, ws, bias))
         # against the float layer: each operand is off by at most half a step of its scale
