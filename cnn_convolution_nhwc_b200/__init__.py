@@ -425,7 +425,7 @@ def _i8_init():
     fast = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(fast)
     fast.bind(*(ctypes.cast(f, _P).value for f in (lib.rmsnorm_i8_fwd, lib.quant_rows_i8_fwd, lib.quant_filter_i8_fwd,
-                                                   lib.dequant_rows_i8_fwd, lib.pointwise_i8_fwd)))
+                                                   lib.dequant_rows_i8_fwd, lib.pointwise_i8_fwd, lib.conv2d_nhwc_fwd_i8)))
     _fast = fast
     return fast
 
@@ -648,6 +648,9 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
     (with norm, float32 [Cin]: after a root-mean-square norm with that weight), times the filter Wq
     int8 [Cout, Cin] with w_scale [Cout] (quant_filter_i8_fwd) -> Y bfloat16 [N,H,W,Cout].
     workspace: a uint8 CUDA tensor of at least conv2d_nhwc_i8_workspace bytes, allocated here if None."""
+    if stream is None and Y is not None and workspace is not None and \
+            _i8_quick((_fast or _i8_init()).layer(X, norm, eps, Wq, w_scale, bias, Y, workspace), "conv2d_nhwc_fwd_i8"):
+        return Y
     import torch
     pw, Cout, Cin2, ldw = _i8_rows(Wq, "Wq")
     px = _tensor(X, torch.bfloat16, 4, "X")

@@ -22,12 +22,15 @@ using FilterFn = int (*)(const void *, int8_t *, float *, int, int, int, int, vo
 using DequantFn = int (*)(const int8_t *, const float *, void *, int, int, int, int, void *);
 using PointwiseFn = int (*)(const int8_t *, const float *, const int8_t *, const float *, const float *, void *, int, int, int,
                             int, int, int, void *);
+using LayerFn = int (*)(const void *, const float *, float, const int8_t *, const float *, const float *, void *, void *, size_t,
+                        int, int, int, int, int, int, void *);
 
 NormFn g_norm;
 RowsFn g_rows;
 FilterFn g_filter;
 DequantFn g_dequant;
 PointwiseFn g_pointwise;
+LayerFn g_layer;
 
 constexpr int64_t kIntMax = 2147483647;
 
@@ -64,6 +67,17 @@ struct Args {
         void *p = matrix(o, r, c, y);
         if (r != rows || c != cols || y != type) ok = false;
         return p;
+    }
+    // A contiguous bfloat16 image batch; `shape` is set, or with `same` compared.
+    void *images(PyObject *o, int64_t (&shape)[4], bool same) {
+        const at::Tensor *t = tensor(o);
+        if (!t || t->dim() != 4 || t->scalar_type() != at::kBFloat16 || !t->is_contiguous()) { ok = false; return nullptr; }
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = t->size(i);
+            if (n > kIntMax || (same && n != shape[i])) ok = false;
+            shape[i] = n;
+        }
+        return t->data_ptr();
     }
     float *floats(PyObject *o, int64_t n) {
         const at::Tensor *t = tensor(o);
@@ -198,10 +212,32 @@ PyObject *pointwise(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// (five addresses: the entry points of the library that the package has loaded)
+// (X, norm or None, eps, Wq, w_scale, bias or None, Y, workspace)
+PyObject *layer(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> int {
+        if (n != 8 || !PyFloat_Check(a[2])) return kAskSlow;
+        Args g;
+        int64_t x[4] = {}, Cout = 0, c = 0;
+        int ldw = 0;
+        void *stream = nullptr;
+        const void *X = g.images(a[0], x, false);
+        const float *norm = a[1] == Py_None ? nullptr : g.floats(a[1], x[3]);
+        const int8_t *w = g.bytes(a[3], Cout, c, ldw);
+        const float *ws = g.floats(a[4], Cout);
+        const float *bias = a[5] == Py_None ? nullptr : g.floats(a[5], Cout);
+        int64_t y[4] = {x[0], x[1], x[2], Cout};
+        void *Y = g.images(a[6], y, true);
+        const at::Tensor *space = g.tensor(a[7]);
+        if (!g.ready(stream) || c != x[3] || !space->is_contiguous()) return kAskSlow;
+        return g_layer(X, norm, (float)PyFloat_AS_DOUBLE(a[2]), w, ws, bias, Y, space->data_ptr(), space->nbytes(), (int)x[0],
+                       (int)x[1], (int)x[2], (int)x[3], (int)Cout, ldw, stream);
+    });
+}
+
+// (six addresses: the entry points of the library that the package has loaded)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    void *p[5] = {};
-    for (Py_ssize_t i = 0; i < n && i < 5; ++i) {
+    void *p[6] = {};
+    for (Py_ssize_t i = 0; i < n && i < 6; ++i) {
         p[i] = PyLong_AsVoidPtr(a[i]);
         if (PyErr_Occurred()) return nullptr;
     }
@@ -210,15 +246,16 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g_filter = reinterpret_cast<FilterFn>(p[2]);
     g_dequant = reinterpret_cast<DequantFn>(p[3]);
     g_pointwise = reinterpret_cast<PointwiseFn>(p[4]);
-    if (!g_norm || !g_rows || !g_filter || !g_dequant || !g_pointwise) {
-        PyErr_SetString(PyExc_ValueError, "bind takes five addresses");
+    g_layer = reinterpret_cast<LayerFn>(p[5]);
+    if (!g_norm || !g_rows || !g_filter || !g_dequant || !g_pointwise || !g_layer) {
+        PyErr_SetString(PyExc_ValueError, "bind takes six addresses");
         return nullptr;
     }
     Py_RETURN_NONE;
 }
 
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {ENTRY(bind), ENTRY(rmsnorm), ENTRY(rows), ENTRY(filter), ENTRY(dequant), ENTRY(pointwise),
+PyMethodDef g_methods[] = {ENTRY(bind), ENTRY(rmsnorm), ENTRY(rows), ENTRY(filter), ENTRY(dequant), ENTRY(pointwise), ENTRY(layer),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding_i8", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -229,6 +229,8 @@ def test_layer_is_its_parts(cb, shape):
         # a workspace for the pitch of 32 bytes, and the smallest one, at 16
         small = torch.empty(N * H * W * ((Cin + 15) // 16 * 16 + 4), dtype=torch.uint8, device="cuda")
         assert torch.equal(Y, cb.conv2d_nhwc_fwd_i8(X, wq, ws, bias, norm=n, eps=1e-5, workspace=small))
+        Y2 = torch.full_like(Y, 7.0)   # every output given: the short call
+        assert cb.conv2d_nhwc_fwd_i8(X, wq, ws, bias, norm=n, eps=1e-5, Y=Y2, workspace=small) is Y2 and torch.equal(Y, Y2)
         q, s = cb.quant_rows_i8_fwd(x) if n is None else cb.rmsnorm_i8_fwd(x, n, eps=1e-5)[:2]
         assert torch.equal(Y.reshape(-1, Cout), cb.pointwise_i8_fwd(q, s, wq, ws, bias))
         # against the float layer: each operand is off by at most half a step of its scale
