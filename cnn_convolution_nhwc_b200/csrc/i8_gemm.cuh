@@ -1,7 +1,8 @@
 // The 1 x 1 convolution (matrix product) in 8-bit integers:
 //     Y[m][n] = (sum_k q[m][k] * Wq[n][k]) * q_scale[m] * w_scale[n] + bias[n]
-// with the sum exact in int32 (|q|, |Wq| <= 128 and at most 131071 terms), the scales and the bias
-// applied in float32 and one rounding to the output type. Both operands run along k, so both are
+// with the sum exact in int32 (|q|, |Wq| <= 128 and at most 131071 terms) and converted to float32,
+// one float32 rounding for the product with q_scale, one for the fused product with w_scale and
+// addition of the bias, and one to the output type; the two kernels round alike. Both operands run along k, so both are
 // staged by plain 2-D tensor copies of 128-byte rows (128 values, 128-byte swizzle) and multiplied
 // by tcgen05.mma kind::i8, K = 32 values a step; rows, columns and k past the matrices read as
 // zeros (the tensor maps' extents are exact), so no size has a special case in the main loop.
@@ -200,11 +201,9 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         constexpr int NB = decltype(nb)::value;
         float v[NB];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) v[i] = static_cast<float>(acc[i]) * s_scale[j + i] * ws;
-        if (p.bias) {
+        for (int i = 0; i < NB; ++i) v[i] = static_cast<float>(acc[i]) * s_scale[j + i];
 #pragma unroll
-            for (int i = 0; i < NB; ++i) v[i] += bias;
-        }
+        for (int i = 0; i < NB; ++i) v[i] = p.bias ? fmaf(v[i], ws, bias) : v[i] * ws;
 #pragma unroll
         for (int i = 0; i < NB; ++i)
             if (has_n && j + i < cols && in_bounds(y0 + 1LL * (j + i) * p.N, 1, y_elems, kSiteI8GemmY, status))
@@ -478,18 +477,20 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 #pragma unroll
                 for (int i = 0; i < UW / 2; ++i)
                     v[i] = f2_pack(static_cast<float>(static_cast<int>(r[2 * i])), static_cast<float>(static_cast<int>(r[2 * i + 1])));
+                // (the sum times its token's scale) times its channel's plus the bias: two roundings with the
+                // conversion's, one more for the fused last step, as in the split kernel
 #pragma unroll
                 for (int i = 0; i < UW / 4; ++i) {
                     const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(s_ws + u * UW + i * 4);
-                    v[2 * i] = f2_mul(f2_mul(v[2 * i], qs), w.x);
-                    v[2 * i + 1] = f2_mul(f2_mul(v[2 * i + 1], qs), w.y);
-                }
-                if (p.bias) {
-#pragma unroll
-                    for (int i = 0; i < UW / 4; ++i) {
-                        const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(s_bias + u * UW + i * 4);
-                        v[2 * i] = f2_add(v[2 * i], w.x);
-                        v[2 * i + 1] = f2_add(v[2 * i + 1], w.y);
+                    v[2 * i] = f2_mul(v[2 * i], qs);
+                    v[2 * i + 1] = f2_mul(v[2 * i + 1], qs);
+                    if (p.bias) {
+                        const ulonglong2 bb = *reinterpret_cast<const ulonglong2 *>(s_bias + u * UW + i * 4);
+                        v[2 * i] = f2_fma(v[2 * i], w.x, bb.x);
+                        v[2 * i + 1] = f2_fma(v[2 * i + 1], w.y, bb.y);
+                    } else {
+                        v[2 * i] = f2_mul(v[2 * i], w.x);
+                        v[2 * i + 1] = f2_mul(v[2 * i + 1], w.y);
                     }
                 }
                 bulk_wait_group_read0();   // the previous unit has left the staging (the leader's store)

@@ -325,8 +325,9 @@ int dequant_rows_i8_fwd(const int8_t *q, const float *scale, void *y, int M, int
  *   Wq, w_scale : 8-bit rows [Cout][ldw] of the filter, float32 [Cout]
  *   bias        : float32 [Cout] or NULL
  *   Y           : dtype [M][Cout], contiguous
- * The sum is exact (int32); scales and bias are applied in float32 in the order written, and the
- * result is rounded once. Bytes of -128 are allowed.
+ * The sum is exact (int32), so a row's result does not depend on the other rows or on M. It is
+ * rounded to float32, multiplied by q_scale, then by w_scale with the bias added in the same
+ * rounding, and rounded to dtype. Bytes of -128 are allowed.
  * Requirements: M, Cin, Cout >= 1; Cin <= 131071 (else CONV_ERR_UNSUPPORTED).
  */
 int pointwise_i8_fwd(const int8_t *q, const float *q_scale, const int8_t *Wq, const float *w_scale,

@@ -191,6 +191,18 @@ def test_product(cb, M, Cin, Cout, variant, monkeypatch):
     assert cb.conv_device_status() == cb.CONV_OK
 
 
+def test_product_rows_do_not_depend_on_the_batch(cb):
+    g = _gen(31)
+    for C, N in ((1000, 776), (4096, 1001)):
+        q, wq = _bytes(g, 1100, C, cb), _bytes(g, N, C, cb)
+        qs, ws, bias = _normal(g, 1100), _normal(g, N), _normal(g, N)
+        for b in (None, bias):
+            for dtype in (torch.bfloat16, torch.float32):
+                y = cb.pointwise_i8_fwd(q, qs, wq, ws, b, dtype=dtype)
+                for M in (1, 20, 100, 300):
+                    assert torch.equal(cb.pointwise_i8_fwd(q[:M], qs[:M], wq, ws, b, dtype=dtype), y[:M])
+
+
 def test_product_largest_sums(cb):
     # 131071 products of -128 * -128: 2^31 - 2^14, the largest sum that is promised
     for M in (3, 700):
