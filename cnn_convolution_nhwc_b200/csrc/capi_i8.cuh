@@ -196,11 +196,16 @@ struct I8Plan {
     int bn, split;
 };
 
-// k blocks of a slot of the split kernel: two, but for the widest tile and where two CTAs share an SM.
+// k blocks of a slot of the split kernel: two, but for the widest tile and the short ring.
 constexpr int i8_slot_kblks(int bn, bool shared) { return bn == 128 || shared ? 1 : 2; }
 
-// Picks the plan whose estimated time (us) is least. The estimate is a start (launch, first copy),
-// an epilogue per round of CTAs, and the larger-than-either sum (hypot) of the k loop and of the
+// Whether the split kernel runs with its short ring, two CTAs on an SM.
+bool i8_shared(int bn, long long ctas, int num_kblk, int split, int num_sms) {
+    return bn <= 32 && (ctas > num_sms || num_kblk <= 8 * split);
+}
+
+// Picks the plan whose estimated time (us) is least. The estimate is a start (launch, first copies;
+// again for each further round of CTAs), an epilogue per round, and the larger-than-either sum (hypot) of the k loop and of the
 // bytes at HBM's rate; a k block takes its own time or what its copies take when every SM's go
 // through L2. The constants are a fit to 2200 measured times on a B200, M 1 .. 2048, N 1024 .. 20480,
 // Cin 512 .. 10240 (rms error 10 %; the plan it picks is on average 1 % slower than the best one
@@ -242,12 +247,12 @@ I8Plan plan_i8(int M, int N, int num_kblk, int num_sms, Clusters clusters) {
             const long long ctas = tiles * S;
             // a split that does not run at once only adds to the work
             if (S > 1 && (ctas > num_sms || 2 * S > num_kblk)) break;
-            const int kb = i8_slot_kblks(bn, bn <= 32 && ctas > num_sms);
+            const int kb = i8_slot_kblks(bn, i8_shared(bn, ctas, num_kblk, S, num_sms));
             const float rounds = static_cast<float>(cdiv(ctas, num_sms));
             const float share = static_cast<float>(cdiv(cdiv(num_kblk, kb), S) * kb);
             const float own = bn == 128 ? 0.177f : bn == 64 ? 0.132f : bn == 32 ? 0.121f : 0.135f;
             const float kblk = fmaxf(own, l2 * (ctas < num_sms ? ctas : num_sms) * (128 + bn));
-            const float t = 2.0f + rounds * (0.019f * cols + (S > 1 ? 0.62f + 0.013f * cols : 0.0f)) +
+            const float t = 0.5f + 1.5f * rounds + rounds * (0.019f * cols + (S > 1 ? 0.62f + 0.013f * cols : 0.0f)) +
                             hypotf(rounds * share * kblk, mbytes / 5.9f);
             if (t < least && (S == 1 || tiles <= clusters(bn, S))) {
                 least = t;
@@ -268,7 +273,6 @@ int i8_split_clusters(DeviceState *d, unsigned bit, int S) {
 template <typename OUT>
 int run_i8_product(const I8Operands &a, I8GemmParams p, cudaStream_t stream, DeviceState *d) {
     constexpr unsigned bit = sizeof(OUT) == 4 ? 148 : 132;
-    // one CTA per SM has the whole shared memory for copies in flight; beyond that two share an SM
     using Split16 = I8SplitCfg<16, 6, i8_slot_kblks(16, false)>;
     using Split32 = I8SplitCfg<32, 5, i8_slot_kblks(32, false)>;
     using Split64 = I8SplitCfg<64, 4, i8_slot_kblks(64, false)>;
@@ -282,7 +286,8 @@ int run_i8_product(const I8Operands &a, I8GemmParams p, cudaStream_t stream, Dev
     if (pl.pair)
         return pl.bn == 256 ? launch_i8_pair<I8PairCfg<256, 5>, OUT>(a, p, stream, d, bit)
                             : launch_i8_pair<I8PairCfg<128, 7>, OUT>(a, p, stream, d, bit + 1);
-    const bool shared = 1LL * ((p.N + 127) / 128) * ((p.M + pl.bn - 1) / pl.bn) * pl.split > d->num_sms;
+    const bool shared = i8_shared(pl.bn, 1LL * ((p.N + 127) / 128) * ((p.M + pl.bn - 1) / pl.bn) * pl.split, p.num_kblk,
+                                  pl.split, d->num_sms);
     switch (pl.bn) {
         case 16:
             return shared ? launch_i8_split<I8SplitCfg<16, 5, i8_slot_kblks(16, true)>, OUT>(a, p, pl.split, stream, d, bit + 3)

@@ -302,6 +302,17 @@ __device__ __forceinline__ void tma_load_2d_if(uint32_t dst, const CUtensorMap *
         : "memory");
 }
 
+// Asks for a box to be brought into L2, without waiting for it or reading it: allowed before
+// grid_dependency_wait, since L2 is where a predecessor's writes arrive.
+__device__ __forceinline__ void tma_prefetch_2d_if(const CUtensorMap *m, int x, int y, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %3, 0;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}"
+        :
+        : "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(leader)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d_if(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z,
                                                uint32_t leader) {
     asm volatile(
