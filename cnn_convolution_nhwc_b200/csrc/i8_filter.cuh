@@ -60,16 +60,18 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
     auto stage = [&](int b0, int b1) {
         const int rows = (b1 - b0 + 3) & ~3;
         if constexpr (VEC) {
-            for (int i = threadIdx.x; i < rows * CHUNKS; i += 256) {
-                const int r = i / CHUNKS, e = (i % CHUNKS) * (16 / static_cast<int>(sizeof(T)));
-                const long long at = 1LL * (b0 + r) * p.Cout + o0 + e;
-                const bool in = b0 + r < b1 && o0 + e < p.Cout &&
-                                in_bounds(at, 16 / sizeof(T), f_elems, kSiteI8FilterF, status);
-                const uint32_t dst = smem_u32(slab) + r * ROW + e * static_cast<int>(sizeof(T));
-                if (in) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(F + at) : "memory");
-                else asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
-            }
-            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            // a thread keeps its 16-byte chunk of the rows and takes every (256 / CHUNKS)-th
+            constexpr int STEP = 256 / CHUNKS, PER = 16 / static_cast<int>(sizeof(T));
+            const int e = (threadIdx.x % CHUNKS) * PER;
+            int r = threadIdx.x / CHUNKS;
+            const T *src = F + 1LL * (b0 + r) * p.Cout + o0 + e;
+            uint32_t dst = smem_u32(slab) + r * ROW + e * static_cast<int>(sizeof(T));
+            const int live = o0 + e < p.Cout ? b1 - b0 : 0;
+#pragma unroll 4
+            for (; r < rows; r += STEP, src += 1LL * STEP * p.Cout, dst += STEP * ROW)
+                cp_async_16(dst, r < live ? src : F,
+                            r < live && in_bounds(src - F, PER, f_elems, kSiteI8FilterF, status) ? 16u : 0u);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
             // a column a lane, eight rows at a time
             const int e = lane;
@@ -104,26 +106,37 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
     };
 
     float top[4] = {0, 0, 0, 0};
+    __nv_bfloat162 top2[2] = {__floats2bfloat162_rn(0.0f, 0.0f), __floats2bfloat162_rn(0.0f, 0.0f)};   // bf16: as they come
     for (int b0 = c0; b0 < c1; b0 += p.piece) {
         const int b1 = c1 - b0 < p.piece ? c1 : b0 + p.piece;
         stage(b0, b1);
-        // two rows at a time: a staged piece ends with a multiple of four, zeros past the last
+        // a staged piece ends with a multiple of four rows, zeros past the last
         const int rows = (b1 - b0 + 3) & ~3;
-        for (int r = 2 * rg; r < rows; r += 64) {
-            uint64_t a0, b0_, a1, b1_;
-            four(r, a0, b0_);
-            four(r + 1, a1, b1_);
-            float l0, h0, l1, h1;
-            f2_split(a0, l0, h0);
-            f2_split(a1, l1, h1);
-            top[0] = max3_abs(top[0], l0, l1);
-            top[1] = max3_abs(top[1], h0, h1);
-            f2_split(b0_, l0, h0);
-            f2_split(b1_, l1, h1);
-            top[2] = max3_abs(top[2], l0, l1);
-            top[3] = max3_abs(top[3], h0, h1);
+#pragma unroll 4
+        for (int r = rg; r < rows; r += 32) {
+            if constexpr (sizeof(T) == 2) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(slab + r * kI8FilterCols + cg);
+                top2[0] = __hmax2_nan(top2[0], __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u.x)));
+                top2[1] = __hmax2_nan(top2[1], __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&u.y)));
+            } else {
+                uint64_t a, b;
+                four(r, a, b);
+                float lo, hi;
+                f2_split(a, lo, hi);
+                top[0] = max3_abs(top[0], lo, 0.0f);
+                top[1] = max3_abs(top[1], hi, 0.0f);
+                f2_split(b, lo, hi);
+                top[2] = max3_abs(top[2], lo, 0.0f);
+                top[3] = max3_abs(top[3], hi, 0.0f);
+            }
         }
         if (!once) __syncthreads();   // the next piece goes where this one was
+    }
+    if constexpr (sizeof(T) == 2) {
+        top[0] = __low2float(top2[0]);
+        top[1] = __high2float(top2[0]);
+        top[2] = __low2float(top2[1]);
+        top[3] = __high2float(top2[1]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -225,22 +238,23 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
             }
         }
         __syncthreads();
+        // a column a warp, a 16-byte chunk a lane
         const int chunks = (b1 - b0 + 15) / 16;
-        for (int i = threadIdx.x; i < kI8FilterCols * chunks; i += 256) {
-            const int col = i / chunks, j = i - col * chunks, o = o0 + col, c = b0 + j * 16;
-            if (o >= p.Cout) break;
-            const uint4 v = *reinterpret_cast<const uint4 *>(tile + static_cast<size_t>(col) * p.piece + (j & ~7) * 16 +
-                                                             (((j & 7) ^ (col >> 2)) << 4));
-            int8_t *dst = p.q + 1LL * o * p.ldq + c;
-            const int n = b1 - c < 16 ? b1 - c : 16;
-            if (!in_bounds(1LL * o * p.Cin + c, n, q_elems, kSiteI8FilterQ, status)) continue;
-            if (n == 16) {
-                *reinterpret_cast<uint4 *>(dst) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int col = warp; col < kI8FilterCols && o0 + col < p.Cout; col += 8) {
+            const uint8_t *from = tile + static_cast<size_t>(col) * p.piece;
+            int8_t *to = p.q + 1LL * (o0 + col) * p.ldq + b0;
+            for (int j = lane; j < chunks; j += 32) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(from + (j & ~7) * 16 + (((j & 7) ^ (col >> 2)) << 4));
+                const int n = b1 - b0 - j * 16 < 16 ? b1 - b0 - j * 16 : 16;
+                if (!in_bounds(1LL * (o0 + col) * p.Cin + b0 + j * 16, n, q_elems, kSiteI8FilterQ, status)) continue;
+                if (n == 16) {
+                    *reinterpret_cast<uint4 *>(to + j * 16) = v;
+                } else {
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int k = 0; k < 15; ++k)
-                    if (k < n) dst[k] = static_cast<int8_t>(w[k >> 2] >> (8 * (k & 3)));
+                    for (int k = 0; k < 15; ++k)
+                        if (k < n) to[j * 16 + k] = static_cast<int8_t>(w[k >> 2] >> (8 * (k & 3)));
+                }
             }
         }
         __syncthreads();

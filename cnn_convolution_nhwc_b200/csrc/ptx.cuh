@@ -280,6 +280,11 @@ __device__ __forceinline__ void tma_load_im2col_4d_pair(uint32_t dst, const CUte
         : "memory");
 }
 
+// Asynchronous 16-byte copy by the calling thread: the first `bytes` (0 to 16) of src, zeros after.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
 // Tensor copies issued by a whole converged warp: only the lane whose `leader` is non-zero arms the
 // barrier and issues them. As with the MMAs, a producer loop that the whole warp runs, with its
 // copies predicated instead of placed under a one-lane branch, issues them faster: measured on
