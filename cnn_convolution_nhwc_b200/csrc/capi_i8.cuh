@@ -8,6 +8,8 @@ namespace convb200 {
 namespace {
 
 constexpr int kI8MaxReduce = 131071;   // (131071 + 1) * 128 * 128 = 2^31: the int32 sums are exact below
+constexpr int kI8MaxCols = 1 << 27;    // of a quantised row: indices past the row's last piece stay in int
+constexpr int kI8MaxRows = 2147483647 - 512;   // of a product and its filter: so do a last tile's rows
 
 int i8_elem(int dtype) { return dtype == CONV_F32 ? 4 : 2; }
 
@@ -34,20 +36,30 @@ int launch_i8_rows(const I8RowsParams &p, int threads, cudaStream_t stream, Devi
 template <typename T, int MODE>
 int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
     // A warp holds rows up to 1024 values (two rows of up to 512: 25088 x 256 took 6.9 us with one,
-    // 4.9 with two, 5.0 with four; 48000 x 512 15.6, 14.5 and 17.0), a block of up to 512
-    // threads rows up to 16384.
+    // 4.9 with two, 5.0 with four; 48000 x 512 15.6, 14.5 and 17.0), a block of up to 512 threads rows
+    // up to 16384. Four groups a thread where a group is one load or the norm's sums keep few blocks
+    // in flight (8192 x 4096 with a residual 42 us with two, 38 with four); two for the gate, whose
+    // arithmetic they do not hide (4096 x 4096: 16.5 us with four, 14.5 with two).
     const int C = p.C;
     if (C % 8 == 0 && aligned(p.x, 16) && aligned(p.residual, 16) && aligned(p.h, 16) && aligned(p.weight, 16)) {
         if (C <= 256) return launch_i8_rows<T, MODE, 1, true, 32, 2, false>(p, 128, stream, d);
         if (C <= 512) return launch_i8_rows<T, MODE, 2, true, 32, 2, false>(p, 128, stream, d);
         if (C <= 1024) return launch_i8_rows<T, MODE, 4, true, 32, 1, false>(p, 128, stream, d);
+        if constexpr (MODE == kI8Glu)
+            if (C <= 8192)
+                return launch_i8_rows<T, MODE, 2, true, 0, 1, false>(p, (C + 511) / 512 * 32, stream, d);
         if (C <= 16384) return launch_i8_rows<T, MODE, 4, true, 0, 1, false>(p, (C + 1023) / 1024 * 32, stream, d);
         return launch_i8_rows<T, MODE, 4, true, 0, 1, true>(p, 512, stream, d);
     }
+    // element by element: 1031 x 5003 in float32 9.9 us with 512 threads and two groups each, 8.3 with
+    // 256 and four, but with two inputs four groups take too many registers
     if (C <= 512) return launch_i8_rows<T, MODE, 2, false, 32, 1, false>(p, 128, stream, d);
     if (C <= 2048) return launch_i8_rows<T, MODE, 2, false, 128, 1, false>(p, 128, stream, d);
     if (C <= 4096) return launch_i8_rows<T, MODE, 2, false, 256, 1, false>(p, 256, stream, d);
-    if (C <= 8192) return launch_i8_rows<T, MODE, 2, false, 512, 1, false>(p, 512, stream, d);
+    if (C <= 8192) {
+        if constexpr (MODE == kI8Plain || MODE == kI8Norm) return launch_i8_rows<T, MODE, 4, false, 256, 1, false>(p, 256, stream, d);
+        else return launch_i8_rows<T, MODE, 2, false, 512, 1, false>(p, 512, stream, d);
+    }
     return launch_i8_rows<T, MODE, 2, false, 512, 1, true>(p, 512, stream, d);
 }
 
@@ -305,7 +317,7 @@ int check_pointwise_i8(const int8_t *q, const float *q_scale, const int8_t *Wq, 
     if (!q || !q_scale || !Wq || !w_scale || !Y) return CONV_ERR_INVALID_ARG;
     if (M < 1 || Cin < 1 || Cout < 1 || (dtype != CONV_BF16 && dtype != CONV_F32)) return CONV_ERR_INVALID_ARG;
     if (ldq < Cin || ldw < Cin) return CONV_ERR_INVALID_ARG;
-    if (Cin > kI8MaxReduce) return CONV_ERR_UNSUPPORTED;
+    if (Cin > kI8MaxReduce || M > kI8MaxRows || Cout > kI8MaxRows) return CONV_ERR_UNSUPPORTED;
     if (int rc = check_i8_rows(q, Cin, ldq)) return rc;
     if (int rc = check_i8_rows(Wq, Cin, ldw)) return rc;
     if (!aligned(q_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 4) || !aligned(Y, i8_elem(dtype)))
@@ -347,6 +359,7 @@ int rmsnorm_i8_fwd(const void *x, const void *residual, const float *weight, voi
         return CONV_ERR_INVALID_ARG;
     const int e = i8_elem(dtype);
     if (int rc = check_i8_rows(q, C, ldq)) return rc;
+    if (C > kI8MaxCols) return CONV_ERR_UNSUPPORTED;
     if (!aligned(x, e) || !aligned(residual, e) || !aligned(h, e) || !aligned(weight, 4) || !aligned(scale, 4))
         return CONV_ERR_MISALIGNED;
     const long long nx = 1LL * M * C * e, nq = i8_extent(M, C, ldq), ns = 4LL * M, nw = 4LL * C;
@@ -370,6 +383,7 @@ int quant_rows_i8_fwd(const void *x, int8_t *q, float *scale, int M, int C, int 
     if (M < 1 || C < 1 || (glu != 0 && glu != 1) || (dtype != CONV_BF16 && dtype != CONV_F32)) return CONV_ERR_INVALID_ARG;
     const int e = i8_elem(dtype);
     if (int rc = check_i8_rows(q, C, ldq)) return rc;
+    if (C > kI8MaxCols) return CONV_ERR_UNSUPPORTED;
     if (!aligned(x, e) || !aligned(scale, 4)) return CONV_ERR_MISALIGNED;
     const long long nx = 1LL * M * C * e * (glu ? 2 : 1), nq = i8_extent(M, C, ldq), ns = 4LL * M;
     if (overlaps(q, nq, x, nx) || overlaps(q, nq, scale, ns) || overlaps(scale, ns, x, nx)) return CONV_ERR_INVALID_ARG;
@@ -384,7 +398,7 @@ int quant_filter_i8_fwd(const void *F, int8_t *Wq, float *scale, int Cin, int Co
                         cudaStream_t stream) {
     if (!F || !Wq || !scale) return CONV_ERR_INVALID_ARG;
     if (Cin < 1 || Cout < 1 || (dtype != CONV_BF16 && dtype != CONV_F32)) return CONV_ERR_INVALID_ARG;
-    if (Cin > kI8MaxReduce) return CONV_ERR_UNSUPPORTED;
+    if (Cin > kI8MaxReduce || Cout > kI8MaxRows) return CONV_ERR_UNSUPPORTED;
     const int e = i8_elem(dtype);
     if (int rc = check_i8_rows(Wq, Cin, ldw)) return rc;
     if (!aligned(F, e) || !aligned(scale, 4)) return CONV_ERR_MISALIGNED;
@@ -409,6 +423,7 @@ int dequant_rows_i8_fwd(const int8_t *q, const float *scale, void *y, int M, int
     if (M < 1 || C < 1 || (dtype != CONV_BF16 && dtype != CONV_F32)) return CONV_ERR_INVALID_ARG;
     const int e = i8_elem(dtype);
     if (int rc = check_i8_rows(q, C, ldq)) return rc;
+    if (C > kI8MaxCols) return CONV_ERR_UNSUPPORTED;
     if (!aligned(y, e) || !aligned(scale, 4)) return CONV_ERR_MISALIGNED;
     const long long ny = 1LL * M * C * e;
     if (overlaps(y, ny, q, i8_extent(M, C, ldq)) || overlaps(y, ny, scale, 4LL * M)) return CONV_ERR_INVALID_ARG;
@@ -422,7 +437,7 @@ int dequant_rows_i8_fwd(const int8_t *q, const float *scale, void *y, int M, int
     while (p.wpr_shift < 3 && (1 << p.wpr_shift) < segs) ++p.wpr_shift;
     const long long blocks = (1LL * M + (8 >> p.wpr_shift) - 1) >> (3 - p.wpr_shift);
     const long long seg_blocks = (segs + (1 << p.wpr_shift) - 1) >> p.wpr_shift;
-    if (blocks > kInt32Max || seg_blocks > 65535) return CONV_ERR_UNSUPPORTED;
+    if (blocks > kInt32Max || seg_blocks > 65535) return CONV_ERR_UNSUPPORTED;   // neither within the limits above
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(seg_blocks));
     cfg.blockDim = dim3(256);
@@ -447,7 +462,7 @@ int pointwise_i8_fwd(const int8_t *q, const float *q_scale, const int8_t *Wq, co
 }
 
 size_t conv2d_nhwc_i8_workspace(int N, int H, int W, int Cin) {
-    if (N < 1 || H < 1 || W < 1 || Cin < 1 || Cin > kI8MaxReduce || 1LL * N * H * W > kInt32Max || 1LL * N * H > kInt32Max)
+    if (N < 1 || H < 1 || W < 1 || Cin < 1 || Cin > kI8MaxReduce || 1LL * N * H > kI8MaxRows || 1LL * N * H * W > kI8MaxRows)
         return 0;
     return 1ull * N * H * W * (conv_i8_row_pitch(Cin) + 4);
 }

@@ -25,6 +25,8 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "ptx.cuh"
 
 namespace convb200 {
@@ -46,8 +48,11 @@ struct I8RowsParams {
 
 __device__ __forceinline__ float i8_to_float(float v) { return v; }
 __device__ __forceinline__ float i8_to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float i8_round_to(float v, float) { return v; }
-__device__ __forceinline__ float i8_round_to(float v, __nv_bfloat16) { return __bfloat162float(__float2bfloat16_rn(v)); }
+template <typename T>
+__device__ __forceinline__ T i8_type(float v) {
+    if constexpr (sizeof(T) == 2) return __float2bfloat16_rn(v);
+    else return v;
+}
 
 // Pairs of float32 in one 64-bit register (sm_100's packed arithmetic: two values an instruction).
 __device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
@@ -138,13 +143,20 @@ __device__ __forceinline__ void i8_pack(const uint64_t (&t)[4], I8Raw<float> &r)
     }
 }
 
-// silu(a) * b in float32, silu(a) = a / (1 + exp(-a)). With e = exp(-|a|) <= 1 the quotient is
-// a * (a < 0 ? e : 1) / (1 + e): nothing overflows and the divisor lies in [1, 2]. The exponential
-// and the quotient are CUDA's fast forms: their relative error (2^-22 + |a| 2^-23) is far below
-// the rounding to 8 bits (2^-8 of the row's largest value) that follows.
-__device__ __forceinline__ float i8_glu(float a, float b) {
-    const float e = __expf(-fabsf(a));
-    return __fdividef(a < 0.0f ? a * e : a, 1.0f + e) * b;
+// silu(a) * b for two pairs in float32, silu(a) = a / (1 + 2^(-a log2 e)), by the fast exponential and
+// reciprocal: relative error below 2^-22 + |a| 2^-24, far below the rounding to 8 bits (2^-8 of
+// the row's largest value) that follows. Gates below -87, whose silu is below 1.5e-36, give 0. With
+// an exponential and a quotient that keep denormals the gate took 14 instructions a value instead
+// of 4, and instructions bound the kernel.
+__device__ __forceinline__ uint64_t i8_glu(uint64_t a, uint64_t b) {
+    float lo, hi;
+    f2_split(f2_mul(a, f2_pack(-1.44269504f, -1.44269504f)), lo, hi);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(lo));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(hi));
+    f2_split(f2_add(f2_pack(lo, hi), f2_pack(1.0f, 1.0f)), lo, hi);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(lo));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(hi));
+    return f2_mul(f2_mul(a, f2_pack(lo, hi)), b);
 }
 
 // What one row's rounding needs: inv = 127 / (A * up), with `up` a power of two that brings rows of
@@ -200,12 +212,11 @@ __device__ __forceinline__ uint32_t i8_bytes(uint32_t a, uint32_t b, uint32_t c,
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// Rounds eight values of a live row, already times `up`, to eight bytes (byte i of the pair of
-// words is value i). BF16: the values are bf16 values.
+// Rounds eight values of a live row, already times `up`, to the low bytes of eight words. BF16: the
+// values are bf16 values.
 template <bool BF16>
-__device__ __forceinline__ uint2 i8_quant8(const uint64_t (&t)[4], const I8RowScale &s) {
+__device__ __forceinline__ void i8_quant8(const uint64_t (&t)[4], const I8RowScale &s, uint32_t (&b)[8]) {
     const uint64_t magic = f2_pack(kI8Magic, kI8Magic);
-    uint32_t b[8];
     if constexpr (BF16) {
         const float below = s.inv * kI8Below, above = s.inv * kI8Above;
         const uint64_t inv0 = f2_pack(below, below), inv1 = f2_pack(above, above);
@@ -245,7 +256,6 @@ __device__ __forceinline__ uint2 i8_quant8(const uint64_t (&t)[4], const I8RowSc
             }
         }
     }
-    return make_uint2(i8_bytes(b[0], b[1], b[2], b[3]), i8_bytes(b[4], b[5], b[6], b[7]));
 }
 
 // One row per group of threads: a block, or a warp (TPR = 32), which takes RW rows at once. A thread
@@ -291,8 +301,8 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
         return Row{e, MODE == kI8Glu ? e + C : e, row * C, row * p.ldq, RW == 1 || row < p.M};
     };
 
-    // column of value i of group k in the piece that starts at c0
-    auto at = [&](int c0, int k, int i) { return VEC ? c0 + (k * tpr + tid) * 8 + i : c0 + (k * 8 + i) * tpr + tid; };
+    // VEC: column of value i of group k in the piece that starts at c0
+    auto at = [&](int c0, int k, int i) { return c0 + (k * tpr + tid) * 8 + i; };
 
     // Reads a piece of the warp's or block's rows: the values t that are rounded; the norms add the
     // squares of h to `sum`. first: the rows' first pass, which writes h.
@@ -321,12 +331,7 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
                 if constexpr (MODE == kI8Glu) {
                     i8_unpack(b[r][k], u);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float g0, g1, u0, u1;
-                        f2_split(t[r][k][i], g0, g1);
-                        f2_split(u[i], u0, u1);
-                        t[r][k][i] = f2_pack(i8_glu(g0, u0), i8_glu(g1, u1));
-                    }
+                    for (int i = 0; i < 4; ++i) t[r][k][i] = i8_glu(t[r][k][i], u[i]);
                 }
                 if constexpr (MODE == kI8NormResidual) {
                     if (first) {
@@ -350,33 +355,38 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
         } else {
             static_assert(VEC || RW == 1, "element accesses: one row");
             const Row row = of(0);
+            const T *from = (from_h ? h : x) + row.x + c0 + tid, *from2 = second + row.second + c0 + tid;
+            const float *weight = p.weight + c0 + tid;
+            const int left = C - c0 - tid;   // element e of the thread is in the row if e * TPR < left
             float a[NV][8], b[NV][8], w[NV][8];
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int c = at(c0, k, i);
-                    const bool in = c < C && in_bounds(row.x + c, 1, x_elems, kSiteI8RowsX, status);
-                    a[k][i] = in ? i8_to_float((from_h ? h : x)[row.x + c]) : 0.0f;
-                    if (two) b[k][i] = in ? i8_to_float(second[row.second + c]) : 0.0f;
-                    if (NORM) w[k][i] = c < C ? p.weight[c] : 0.0f;
+                    const int e = (k * 8 + i) * TPR;
+                    const bool in = e < left && in_bounds(row.x + c0 + tid + e, 1, x_elems, kSiteI8RowsX, status);
+                    a[k][i] = in ? i8_to_float(from[e]) : 0.0f;
+                    if (two) b[k][i] = in ? i8_to_float(from2[e]) : 0.0f;
+                    if (NORM) w[k][i] = in ? weight[e] : 0.0f;
                 }
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int c = at(c0, k, i);
-                    if constexpr (MODE == kI8Glu) a[k][i] = i8_glu(a[k][i], b[k][i]);
-                    if constexpr (MODE == kI8NormResidual) {
-                        if (first) {
-                            a[k][i] = i8_round_to(a[k][i] + b[k][i], T());
-                            if (c < C) h[row.x + c] = static_cast<T>(a[k][i]);
-                        }
-                    }
-                }
-#pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     t[0][k][i] = f2_pack(a[k][2 * i], a[k][2 * i + 1]);
+                    if constexpr (MODE == kI8Glu) t[0][k][i] = i8_glu(t[0][k][i], f2_pack(b[k][2 * i], b[k][2 * i + 1]));
+                    if constexpr (MODE == kI8NormResidual) {
+                        if (first) {
+                            float lo, hi;
+                            f2_split(f2_add(t[0][k][i], f2_pack(b[k][2 * i], b[k][2 * i + 1])), lo, hi);
+                            const T hlo = i8_type<T>(lo), hhi = i8_type<T>(hi);
+                            const int e = (k * 8 + 2 * i) * TPR;
+                            T *to = h + row.x + c0 + tid;
+                            if (e < left) to[e] = hlo;
+                            if (e + TPR < left) to[e + TPR] = hhi;
+                            t[0][k][i] = f2_pack(i8_to_float(hlo), i8_to_float(hhi));
+                        }
+                    }
                     if constexpr (NORM) {
                         sum[0] = f2_fma(t[0][k][i], t[0][k][i], sum[0]);
                         t[0][k][i] = f2_mul(t[0][k][i], f2_pack(w[k][2 * i], w[k][2 * i + 1]));
@@ -385,19 +395,27 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
             }
         }
     };
-    auto store = [&](int c0, int r, int k, uint2 b) {
+    auto store = [&](int c0, int r, int k, const uint32_t (&b)[8]) {
         const Row row = of(r);
-        int8_t *q = p.q + row.q;
         if constexpr (VEC) {
             const int c = at(c0, k, 0);
-            if (c < C && row.live && in_bounds(row.h + c, 8, n_elems, kSiteI8RowsQ, status)) *reinterpret_cast<uint2 *>(q + c) = b;
+            if (c < C && row.live && in_bounds(row.h + c, 8, n_elems, kSiteI8RowsQ, status))
+                *reinterpret_cast<uint2 *>(p.q + row.q + c) =
+                    make_uint2(i8_bytes(b[0], b[1], b[2], b[3]), i8_bytes(b[4], b[5], b[6], b[7]));
         } else {
+            int8_t *to = p.q + row.q + c0 + tid;
+            const int left = C - c0 - tid;
+            auto group = [&](auto all) {
+                constexpr bool ALL = decltype(all)::value;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int c = at(c0, k, i);
-                if (c < C && in_bounds(row.h + c, 1, n_elems, kSiteI8RowsQ, status))
-                    q[c] = static_cast<int8_t>((i < 4 ? b.x : b.y) >> (8 * (i & 3)));
-            }
+                for (int i = 0; i < 8; ++i) {
+                    const int e = (k * 8 + i) * TPR;
+                    if ((ALL || e < left) && in_bounds(row.h + c0 + tid + e, 1, n_elems, kSiteI8RowsQ, status))
+                        to[e] = static_cast<int8_t>(b[i]);
+                }
+            };
+            if (C - c0 >= (k + 1) * 8 * TPR) group(std::true_type());
+            else group(std::false_type());
         }
     };
 
@@ -446,10 +464,9 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
             const int warps = tpr >> 5;
             amax = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
             if constexpr (NORM) {
-                sum = lane < warps ? s_sum[lane] : 0.0f;
+                sum = lane < warps ? s_sum[lane] : 0.0f;   // lanes 16 .. 31 hold zeros
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                sum = __shfl_sync(0xffffffffu, sum, 0);
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             }
         }
         const bool finite = amax < 0x7f800000u && (!NORM || sum < __uint_as_float(0x7f800000u));
@@ -474,7 +491,9 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) t[r][k][i] = f2_mul(t[r][k][i], f2_pack(s[r].up, s[r].up));
             }
-            store(c0, r, k, s[r].dead ? make_uint2(0u, 0u) : i8_quant8<BF16>(t[r][k], s[r]));
+            uint32_t b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (!s[r].dead) i8_quant8<BF16>(t[r][k], s[r], b);
+            store(c0, r, k, b);
         }
         if (C - c0 <= piece) break;
     }

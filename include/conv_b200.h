@@ -270,11 +270,15 @@ int dwpw_fwd(const float *x, const float *w_dw, const float *b_dw, const void *F
  * of zeros has q = 0 and scale = 0. A row with a NaN or an infinity in v has q = 0 and scale = NaN,
  * and so everything computed from it is NaN.
  *
- * Rules for all of them, besides the common ones: M (rows) and C may be of any size whose rows fit
- * (offsets are 64-bit); dtype is a conv_dtype (other values: CONV_ERR_INVALID_ARG); a pitch below
- * the row's length is CONV_ERR_INVALID_ARG, a pitch or a row pointer off the 16-byte rule
- * CONV_ERR_MISALIGNED; other pointers are aligned to their element. Results do not depend on the
- * shape of the launch: no atomics, one order per sum (integers in the product).
+ * Rules for all of them, besides the common ones: offsets are 64-bit, so tensors may pass 2^31
+ * elements; rows of up to 2^27 values are quantised and read back, products and filters have up to
+ * 2^31 - 513 rows (beyond: CONV_ERR_UNSUPPORTED). dtype is a conv_dtype (other values:
+ * CONV_ERR_INVALID_ARG); a pitch below the row's length is CONV_ERR_INVALID_ARG, a pitch or a row
+ * pointer off the 16-byte rule CONV_ERR_MISALIGNED; other pointers are aligned to their element
+ * (16-byte aligned tensors are faster). There are no atomics: the sum of squares of a norm has an
+ * order that C and the pointers' alignment fix, every other result does not depend on the launch.
+ * conv_last_kernel() afterwards names i8_rows_kernel, i8_filter_kernel, i8_dequant_kernel,
+ * i8_split_kernel (few tokens) or i8_pair_kernel.
  */
 typedef enum {
     CONV_BF16 = 0,
@@ -301,7 +305,8 @@ int rmsnorm_i8_fwd(const void *x, const void *residual, const float *weight, voi
 /*
  * 8-bit rows of activations: v = x (glu = 0, x is dtype [M][C]), or the gated product of a
  * feed-forward pair (glu = 1, x is dtype [M][2C], its halves gate and up):
- *     v[c] = silu(x[c]) * x[C + c],  silu(a) = a / (1 + exp(-a)), in float32.
+ *     v[c] = silu(x[c]) * x[C + c],  silu(a) = a / (1 + exp(-a)), in float32 (relative error below
+ * 2^-22 + |a| 2^-24; gates below -87, whose silu is below 1.5e-36 in magnitude, give 0).
  * Also quantises a filter stored [Cout][Cin] (a row per output channel).
  */
 int quant_rows_i8_fwd(const void *x, int8_t *q, float *scale, int M, int C, int ldq, int glu, int dtype,
@@ -345,7 +350,7 @@ int pointwise_i8_fwd(const int8_t *q, const float *q_scale, const int8_t *Wq, co
  *               conv2d_nhwc_i8_workspace() bytes hold the rows at conv_i8_row_pitch(Cin);
  *               N*H*W * (Cin rounded up to 16, plus 4) bytes are enough. Calls that may run at
  *               the same time (different streams) need one each.
- * eps is ignored without norm. Requirements: N, H, W, Cin, Cout >= 1; N*H*W below 2^31 and
+ * eps is ignored without norm. Requirements: N, H, W, Cin, Cout >= 1; N*H*W <= 2^31 - 513 and
  * Cin <= 131071 (else CONV_ERR_UNSUPPORTED).
  */
 size_t conv2d_nhwc_i8_workspace(int N, int H, int W, int Cin);   /* 0 if invalid or unsupported */

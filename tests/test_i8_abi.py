@@ -65,6 +65,7 @@ def test_rmsnorm_rejects(args, code):
     ((X, off(X, 96), S, 2, 20, 32, 1, BF16), INV),   # inside the second half of the gated rows
     ((X, Q, off(X, 152), 2, 20, 32, 1, BF16), INV),
     ((X, Q, off(S, 2), 2, 20, 32, 0, BF16), MIS),
+    ((X, Q, S, 1, 2 ** 27 + 1, 2 ** 27 + 16, 0, BF16), UNS),
 ])
 def test_quant_rows_rejects(args, code):
     assert cb.lib.quant_rows_i8_fwd(*args, None) == code
@@ -92,6 +93,7 @@ def test_quant_filter_rejects(args, code):
     ((Q, S, Q, 2, 20, 32, BF16), INV),
     ((Q, S, Y, 0, 20, 32, BF16), INV),
     ((Q, S, off(Y, 1), 2, 20, 32, BF16), MIS),
+    ((Q, S, Y, 1, 2 ** 27 + 1, 2 ** 27 + 16, BF16), UNS),
 ])
 def test_dequant_rejects(args, code):
     assert cb.lib.dequant_rows_i8_fwd(*args, None) == code
@@ -112,6 +114,8 @@ def test_dequant_rejects(args, code):
     ((Q, S, W, R, off(B, 1), Y, 2, 20, 8, 32, 32, BF16), MIS),
     ((Q, S, W, R, B, off(Y, 2), 2, 20, 8, 32, 32, F32), MIS),
     ((Q, S, W, R, B, Y, 2, 131072, 8, 131072, 131072, BF16), UNS),
+    ((Q, S, W, R, B, Y, 2 ** 31 - 512, 20, 8, 32, 32, BF16), UNS),
+    ((Q, S, W, R, B, Y, 2, 20, 2 ** 31 - 512, 32, 32, BF16), UNS),
     ((Q, S, W, R, B, Q, 2, 20, 8, 32, 32, BF16), INV),
     ((Q, S, W, R, Y, Y, 2, 20, 8, 32, 32, BF16), INV),
     ((Q, S, W, R, B, Y, 2, 20, 8, 32, 32, 5), INV),
