@@ -386,6 +386,44 @@ def test_tensors_off_16_bytes(cb, M, C, dtype):
             del os.environ["CONV_B200_I8"]
 
 
+def test_gates_far_from_zero(cb):
+    # silu against float64 over the float32 range of gates; below -87 it counts as 0 (its size is below 1.5e-36)
+    gates = torch.tensor([-3e38, -1e30, -200.0, -100.0, -88.0, -87.5, -86.0, -60.0, -20.0, -5.0, -1.0, -0.0, 0.0, 1e-30, 0.5, 5.0, 20.0,
+                          88.0, 100.0, 1e30], device="cuda")
+    for up in (1.0, -0.37):
+        for g in gates:   # a row each, so that its own value sets the scale
+            x = torch.stack([g.repeat(8), torch.full((8,), up, device="cuda")]).reshape(1, 16)
+            q, s = cb.quant_rows_i8_fwd(x, glu=True)
+            v, got = ref.glu(x)[0, 0], float(q[0, 0].item() * s[0].double().item())
+            assert abs(got - v) <= (2.0 ** -21 + abs(float(g)) * 2.0 ** -23 if abs(float(g)) < 100 else 2.0 ** -21) * abs(v) + 1.5e-36 * abs(up)
+
+
+def test_rows_of_2_27_values(cb):
+    for C in (1 << 27, (1 << 27) - 3):
+        x = torch.zeros(1, C, dtype=torch.bfloat16, device="cuda")
+        x[0, 5], x[0, C - 1], x[0, C - 20] = 2.0, -1.0, 0.5
+        q, s = cb.quant_rows_i8_fwd(x)
+        assert s.item() == float(np.float32(2.0) / np.float32(127.0)) and int(q.int().abs().sum(dtype=torch.int64)) == 127 + 64 + 32
+        assert q[0, 5] == 127 and q[0, C - 1] == -64 and q[0, C - 20] == 32   # -63.5 to even
+        y = cb.dequant_rows_i8_fwd(q, s)
+        assert y[0, C - 1] == (torch.tensor(-64.0) * s.cpu()).bfloat16().item() and int((y != 0).sum()) == 3
+
+
+def test_rows_past_the_batch_are_left_alone(cb):
+    g = _gen(14)
+    for M, C in ((3, 1000), (5, 257), (1, 4096)):
+        buf = torch.full((M + 2, C), 9.0, dtype=torch.bfloat16, device="cuda")
+        scale = torch.full((M + 2,), 9.0, device="cuda")
+        x, r = _normal(g, M, C, dtype=torch.bfloat16), _normal(g, M, C, dtype=torch.bfloat16)
+        cb.rmsnorm_i8_fwd(x, torch.ones(C, device="cuda"), r, h=buf[1:M + 1] if (C * 2) % 16 == 0 else buf[:M], scale=scale[1:M + 1])
+        first = 1 if (C * 2) % 16 == 0 else 0
+        assert torch.all(buf[:first] == 9.0) and torch.all(buf[M + first:] == 9.0) and scale[0] == 9.0 and scale[M + 1] == 9.0
+        q, s = cb.quant_rows_i8_fwd(x)
+        y = torch.full((M + 1, C), 9.0, device="cuda")
+        cb.dequant_rows_i8_fwd(q, s, y=y[:M])
+        assert torch.all(y[M] == 9.0)
+
+
 CHILD = r'''
 import os, sys
 import numpy as np
