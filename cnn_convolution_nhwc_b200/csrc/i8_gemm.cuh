@@ -17,7 +17,6 @@
 #include "dense_tc.cuh"
 #include "dense_halo.cuh"
 #include "i8_rows.cuh"
-#include "ptx.cuh"
 
 namespace convb200 {
 

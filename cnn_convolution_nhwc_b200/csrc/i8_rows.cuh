@@ -27,7 +27,7 @@
 
 #include <type_traits>
 
-#include "ptx.cuh"
+#include "i8_ptx.cuh"
 
 namespace convb200 {
 
