@@ -177,7 +177,7 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
         if (rank == 0 && threadIdx.x < 8 && o < p.Cout && in_bounds(o, 1, p.Cout, kSiteI8FilterScale, status))
             p.scale[o] = finite ? __uint_as_float(m) / 127.0f : __uint_as_float(0x7fc00000u);
     }
-    cluster_sync_all();   // nobody leaves while its maxima may still be read
+    cluster_arrive();   // these maxima have been read; nobody leaves before all have (cluster_wait below)
 
     // bf16: the two sides of inv (i8_rows.cuh); float32: inv
     constexpr bool BF16 = sizeof(T) == 2;
@@ -202,19 +202,17 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
                 four(g * 4 + j, t[0], t[1]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint64_t u = f2_fma(t[i], inv0[i], magic);
-                    float lo, hi, lo1, hi1;
-                    f2_split(u, lo, hi);
+                    float lo, hi;
                     if constexpr (BF16) {
-                        f2_split(f2_fma(t[i], inv1[i], magic), lo1, hi1);
-                        m[j][2 * i] = i8_even(lo, lo1);
-                        m[j][2 * i + 1] = i8_even(hi, hi1);
+                        f2_split(i8_round_bf16(t[i], inv0[i], inv1[i]), lo, hi);
                     } else {
-                        f2_split(f2_fma(t[i], inv0[i], f2_fma(u, minus1, magic)), lo1, hi1);
-                        worst = max3_abs(worst, lo1, hi1);
-                        m[j][2 * i] = __float_as_uint(lo);
-                        m[j][2 * i + 1] = __float_as_uint(hi);
+                        const uint64_t u = f2_fma(t[i], inv0[i], magic);
+                        f2_split(f2_fma(t[i], inv0[i], f2_fma(u, minus1, magic)), lo, hi);
+                        worst = max3_abs(worst, lo, hi);
+                        f2_split(u, lo, hi);
                     }
+                    m[j][2 * i] = __float_as_uint(lo);
+                    m[j][2 * i + 1] = __float_as_uint(hi);
                 }
             }
             if (!plain || (!BF16 && worst > kI8NearHalf)) {
@@ -259,6 +257,7 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
         }
         __syncthreads();
     }
+    cluster_wait();
 }
 
 struct I8DequantParams {

@@ -17,7 +17,7 @@
 // taken exactly (a product's rounded part and its error, and two fused multiply-adds). Where v and
 // A are bf16 values, exact halves are common (about one value in 300) and nothing else comes
 // nearer to a half than 1.5e-5 relative: there v * inv (1 - 2^-20) and v * inv (1 + 2^-20) round
-// apart on exact halves only, and the even one is taken, without a branch.
+// apart on exact halves only, and the even one is taken by the rounding of their sum.
 //
 // A row with A = 0 has q = 0 and scale = 0. A row that holds a NaN or an infinity (after the
 // gate, the residual and the weight), or whose sum of squares passes the float32 range, has
@@ -201,10 +201,12 @@ __device__ __forceinline__ uint32_t i8_quant1(float t, const I8RowScale &s) {
     return i8_settle(v, fmaf(v, s.inv, kI8Magic), s);
 }
 
-// The even one of two neighbouring integers, or the common value of two equal ones.
-__device__ __forceinline__ uint32_t i8_even(float a, float b) {
-    const uint32_t u = __float_as_uint(a);
-    return (u & 1u) ? __float_as_uint(b) : u;
+// bf16 values t and their inv * (1 -+ 2^-20): magic + k from both sides are equal, or neighbours on
+// an exact half. Their sum lies in [2^24, 2^25), where float32 holds even integers only: it is 2
+// (magic + k), and on a half rounds to the k that is even. Its low mantissa bits are k's.
+__device__ __forceinline__ uint64_t i8_round_bf16(uint64_t t, uint64_t below, uint64_t above) {
+    const uint64_t magic = f2_pack(kI8Magic, kI8Magic);
+    return f2_add(f2_fma(t, below, magic), f2_fma(t, above, magic));
 }
 
 // The low bytes of four words.
@@ -216,20 +218,18 @@ __device__ __forceinline__ uint32_t i8_bytes(uint32_t a, uint32_t b, uint32_t c,
 // values are bf16 values.
 template <bool BF16>
 __device__ __forceinline__ void i8_quant8(const uint64_t (&t)[4], const I8RowScale &s, uint32_t (&b)[8]) {
-    const uint64_t magic = f2_pack(kI8Magic, kI8Magic);
     if constexpr (BF16) {
         const float below = s.inv * kI8Below, above = s.inv * kI8Above;
         const uint64_t inv0 = f2_pack(below, below), inv1 = f2_pack(above, above);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float lo0, hi0, lo1, hi1;
-            f2_split(f2_fma(t[i], inv0, magic), lo0, hi0);
-            f2_split(f2_fma(t[i], inv1, magic), lo1, hi1);
-            b[2 * i] = i8_even(lo0, lo1);
-            b[2 * i + 1] = i8_even(hi0, hi1);
+            float lo, hi;
+            f2_split(i8_round_bf16(t[i], inv0, inv1), lo, hi);
+            b[2 * i] = __float_as_uint(lo);
+            b[2 * i + 1] = __float_as_uint(hi);
         }
     } else {
-        const uint64_t inv = f2_pack(s.inv, s.inv), minus1 = f2_pack(-1.0f, -1.0f);
+        const uint64_t magic = f2_pack(kI8Magic, kI8Magic), inv = f2_pack(s.inv, s.inv), minus1 = f2_pack(-1.0f, -1.0f);
         uint64_t m[4];
         float worst = 0.0f;
 #pragma unroll
