@@ -446,6 +446,12 @@ def _i8_quick(rc, what):
     return False
 
 
+def _i8_sizes(name, *sizes):
+    """The C ABI's sizes are int: larger ones must not be cut to their low bits on the way."""
+    if max(sizes) > 2 ** 31 - 1:
+        raise ValueError(f"{name} is larger than 2^31 - 1 in a dimension")
+
+
 def _i8_matrix(x, name):
     """(conv_dtype, address) of a contiguous bfloat16 or float32 CUDA matrix."""
     import torch
@@ -456,6 +462,7 @@ def _i8_matrix(x, name):
     if x.dtype is not _BF16 and x.dtype is not _F32:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {x.dtype}")
     _tensor(x, x.dtype, 2, name)
+    _i8_sizes(name, *x.shape)
     return CONV_BF16 if x.dtype is _BF16 else CONV_F32, x.data_ptr()
 
 
@@ -484,6 +491,7 @@ def _i8_rows(t, name):
     pitch, step = t.stride()
     if n < 2:
         pitch = (c + 15) // 16 * 16   # the stride of a dimension with one element means nothing
+    _i8_sizes(name, n, c, pitch)
     if (step != 1 and c > 1) or pitch < c or pitch % 16:
         raise ValueError(f"{name} must be an int8 matrix whose rows are contiguous and start on 16-byte boundaries "
                          "(empty_rows_i8 makes one)")
@@ -495,6 +503,7 @@ def empty_rows_i8(rows, C, device="cuda"):
     [rows, pitch] whose rows start where conv_i8_row_pitch puts them. Copy 8-bit rows from
     elsewhere (a checkpoint's filter) into one with copy_()."""
     import torch
+    _i8_sizes("the matrix", int(rows), int(C))
     pitch = lib.conv_i8_row_pitch(int(C))
     if pitch == 0 or rows < 1:
         raise ValueError("rows and C must be positive")
@@ -655,6 +664,7 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
     pw, Cout, Cin2, ldw = _i8_rows(Wq, "Wq")
     px = _tensor(X, torch.bfloat16, 4, "X")
     N, H, W, Cin = X.shape
+    _i8_sizes("X", N, H, W, Cin)
     if Cin2 != Cin:
         raise ValueError(f"Wq must have X's {Cin} channels, got {Cin2}")
     pws = _i8_ptr(w_scale, _F32, (Cout,), "w_scale")

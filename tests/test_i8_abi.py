@@ -168,3 +168,10 @@ def test_binding_checks():
         cb.empty_rows_i8(0, 8, device="cpu")
     e = cb.empty_rows_i8(3, 20, device="cpu")
     assert e.shape == (3, 20) and e.stride() == (32, 1)
+
+
+def test_sizes_past_int_are_not_cut():
+    with pytest.raises(ValueError, match="larger than 2"):
+        cb.empty_rows_i8(2 ** 32 + 4, 8, device="meta")
+    with pytest.raises(ValueError, match="larger than 2"):
+        cb.empty_rows_i8(1, 2 ** 32 + 8, device="meta")

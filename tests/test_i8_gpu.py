@@ -521,3 +521,31 @@ def test_binding_refuses_with_the_outputs_given(cb):
         cb.dequant_rows_i8_fwd(memory.view(torch.int8)[:128].view(4, 32), scale, y=memory.view(4, 32))
     with pytest.raises(cb.ConvError):
         cb.rmsnorm_i8_fwd(x, w, eps=0.0, q=q, scale=scale)
+
+
+def test_binding_does_not_cut_sizes_past_int(cb):
+    """2^32 + 16 columns or rows, 16 in an int's bits: refused before anything is launched."""
+    n = 2 ** 32 + 16
+    x = torch.empty(1, n, dtype=torch.int8, device="cuda")
+    one = torch.ones(1, device="cuda")
+    y = torch.full((1, 16), 5.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="larger than 2"):
+        cb.dequant_rows_i8_fwd(x, one, y=y)
+    with pytest.raises(ValueError, match="larger than 2"):
+        cb.pointwise_i8_fwd(x, one, x, one, y=y[:, :1].contiguous())
+    assert torch.all(y == 5.0)
+    del x
+    x = torch.empty(n // 2, 2, dtype=torch.bfloat16, device="cuda")   # 2^31 + 8 rows
+    q, scale = cb.empty_rows_i8(16, 2), torch.full((16,), 5.0, device="cuda")
+    for glu in (False, True):
+        with pytest.raises(ValueError, match="larger than 2"):
+            cb.quant_rows_i8_fwd(x, glu=glu, q=q, scale=scale)
+        with pytest.raises(ValueError, match="larger than 2"):
+            cb.quant_rows_i8_fwd(x, glu=glu)
+    with pytest.raises(ValueError, match="larger than 2"):
+        cb.rmsnorm_i8_fwd(x, torch.ones(2, device="cuda"), q=q, scale=scale)
+    with pytest.raises(ValueError, match="larger than 2"):
+        cb.quant_filter_i8_fwd(x, q=q, scale=scale)
+    with pytest.raises(ValueError, match="larger than 2"):
+        cb.conv2d_nhwc_fwd_i8(x.view(n // 2, 1, 1, 2), cb.empty_rows_i8(16, 2), scale)
+    assert torch.all(scale == 5.0)
