@@ -11,6 +11,8 @@ constexpr int kI8MaxReduce = 131071;   // (131071 + 1) * 128 * 128 = 2^31: the i
 constexpr int kI8MaxCols = 1 << 27;    // of a quantised row: indices past the row's last piece stay in int
 constexpr int kI8MaxRows = 2147483647 - 512;   // of a product and its filter: so do a last tile's rows
 
+constexpr int kI8StagedMax = 220 * 1024;   // bytes of a row in the shared memory of a block that has an SM alone
+
 int i8_elem(int dtype) { return dtype == CONV_F32 ? 4 : 2; }
 
 // Bytes from the first to past the last value of `rows` rows of C bytes, ld apart.
@@ -33,6 +35,19 @@ int launch_i8_rows(const I8RowsParams &p, int threads, cudaStream_t stream, Devi
     return launched(launch_k(cfg, i8_rows_kernel<T, MODE, NV, VEC, TPR, RW, STREAM>, p, d->status), "i8_rows_kernel");
 }
 
+template <typename T, int MODE, int TPR>
+int launch_i8_staged(const I8RowsParams &p, int bytes, cudaStream_t stream, DeviceState *d) {
+    auto kern = i8_rows_staged_kernel<T, MODE, TPR>;
+    constexpr unsigned bit = 160 + (sizeof(T) == 4 ? 12 : 0) + MODE * 3 + (TPR == 128 ? 0 : TPR == 256 ? 1 : 2);
+    if (int rc = ensure_smem_attr(d, bit, kern, kI8StagedMax)) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.M));
+    cfg.blockDim = dim3(TPR);
+    cfg.dynamicSmemBytes = static_cast<size_t>(bytes);
+    cfg.stream = stream;
+    return launched(launch_k(cfg, kern, p, d->status), "i8_rows_staged_kernel");
+}
+
 template <typename T, int MODE>
 int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
     // A warp holds rows up to 1024 values (two rows of up to 512: 25088 x 256 took 6.9 us with one,
@@ -45,20 +60,40 @@ int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
         if (C <= 256) return launch_i8_rows<T, MODE, 1, true, 32, 2, false>(p, 128, stream, d);
         if (C <= 512) return launch_i8_rows<T, MODE, 2, true, 32, 2, false>(p, 128, stream, d);
         if (C <= 1024) return launch_i8_rows<T, MODE, 4, true, 32, 1, false>(p, 128, stream, d);
-        if constexpr (MODE == kI8Glu)
+        if constexpr (MODE == kI8Glu) {
             if (C <= 8192)
                 return launch_i8_rows<T, MODE, 2, true, 0, 1, false>(p, (C + 511) / 512 * 32, stream, d);
+            // three groups (56 registers a thread) unless four (64) let more rows be on an SM: 8192 x 9216
+            // in bf16 60.6 us with three and 67.2 with four, 8192 x 10240 80.1 and 71.7
+            const int threads = (C + 767) / 768 * 32, threads4 = (C + 1023) / 1024 * 32;
+            if (C <= 12288 && 65536 / (threads * 56) >= 65536 / (threads4 * 64))
+                return launch_i8_rows<T, MODE, 3, true, 0, 1, false>(p, threads, stream, d);
+        }
         if (C <= 16384) return launch_i8_rows<T, MODE, 4, true, 0, 1, false>(p, (C + 1023) / 1024 * 32, stream, d);
         return launch_i8_rows<T, MODE, 4, true, 0, 1, true>(p, 512, stream, d);
     }
-    // element by element: 1031 x 5003 in float32 9.9 us with 512 threads and two groups each, 8.3 with
-    // 256 and four, but with two inputs four groups take too many registers
+    // Element by element: in registers up to 2048 values (8192 x 901: 16.4 us with 128 threads a row, 11.4
+    // with a warp), in float32 up to 8192 (1031 x 5003 10.1 us, staged 10.6; with a residual 15.4 and 17.0;
+    // two inputs at four groups a thread would take too many registers); beyond that staged (bf16: 8192 x
+    // 4095 30.4 us in registers, 20.3 staged; 4096 x 12343 77.6 streamed, 28.0 staged), in float32 while two
+    // blocks fit on an SM (1024 x 17001 27.6 us streamed, 17.2 staged; 1024 x 30001 38.2 and 41.3), in bf16
+    // while one does (1024 x 60001 82.6 and 50.7).
     if (C <= 512) return launch_i8_rows<T, MODE, 2, false, 32, 1, false>(p, 128, stream, d);
+    if (C <= 1024) return launch_i8_rows<T, MODE, 4, false, 32, 1, false>(p, 128, stream, d);
     if (C <= 2048) return launch_i8_rows<T, MODE, 2, false, 128, 1, false>(p, 128, stream, d);
-    if (C <= 4096) return launch_i8_rows<T, MODE, 2, false, 256, 1, false>(p, 256, stream, d);
-    if (C <= 8192) {
-        if constexpr (MODE == kI8Plain || MODE == kI8Norm) return launch_i8_rows<T, MODE, 4, false, 256, 1, false>(p, 256, stream, d);
-        else return launch_i8_rows<T, MODE, 2, false, 512, 1, false>(p, 512, stream, d);
+    if constexpr (sizeof(T) == 4) {
+        if (C <= 4096) return launch_i8_rows<T, MODE, 2, false, 256, 1, false>(p, 256, stream, d);
+        if (C <= 8192) {
+            if constexpr (MODE == kI8Plain || MODE == kI8Norm) return launch_i8_rows<T, MODE, 4, false, 256, 1, false>(p, 256, stream, d);
+            else return launch_i8_rows<T, MODE, 2, false, 512, 1, false>(p, 512, stream, d);
+        }
+    }
+    const long long bytes = 1LL * i8_staged_bytes<T>(MODE == kI8Glu ? 2 * C : C) * (MODE == kI8NormResidual ? 2 : 1);
+    if (bytes <= (sizeof(T) == 4 ? kI8StagedMax / 2 : kI8StagedMax)) {
+        const int n = static_cast<int>(bytes);
+        if (C <= 4096) return launch_i8_staged<T, MODE, 128>(p, n, stream, d);
+        if (C <= 16384) return launch_i8_staged<T, MODE, 256>(p, n, stream, d);
+        return launch_i8_staged<T, MODE, 512>(p, n, stream, d);
     }
     return launch_i8_rows<T, MODE, 2, false, 512, 1, true>(p, 512, stream, d);
 }

@@ -27,6 +27,7 @@
 
 #include <type_traits>
 
+#include "depthwise_plane.cuh"   // bulk_g2s
 #include "i8_ptx.cuh"
 
 namespace convb200 {
@@ -214,15 +215,15 @@ __device__ __forceinline__ uint32_t i8_bytes(uint32_t a, uint32_t b, uint32_t c,
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// Rounds eight values of a live row, already times `up`, to the low bytes of eight words. BF16: the
-// values are bf16 values.
-template <bool BF16>
-__device__ __forceinline__ void i8_quant8(const uint64_t (&t)[4], const I8RowScale &s, uint32_t (&b)[8]) {
+// Rounds the NP pairs of values of a live row, already times `up`, to the low bytes of words. BF16:
+// the values are bf16 values.
+template <bool BF16, int NP>
+__device__ __forceinline__ void i8_quant(const uint64_t (&t)[NP], const I8RowScale &s, uint32_t (&b)[2 * NP]) {
     if constexpr (BF16) {
         const float below = s.inv * kI8Below, above = s.inv * kI8Above;
         const uint64_t inv0 = f2_pack(below, below), inv1 = f2_pack(above, above);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NP; ++i) {
             float lo, hi;
             f2_split(i8_round_bf16(t[i], inv0, inv1), lo, hi);
             b[2 * i] = __float_as_uint(lo);
@@ -230,17 +231,17 @@ __device__ __forceinline__ void i8_quant8(const uint64_t (&t)[4], const I8RowSca
         }
     } else {
         const uint64_t magic = f2_pack(kI8Magic, kI8Magic), inv = f2_pack(s.inv, s.inv), minus1 = f2_pack(-1.0f, -1.0f);
-        uint64_t m[4];
+        uint64_t m[NP];
         float worst = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NP; ++i) {
             m[i] = f2_fma(t[i], inv, magic);
             float lo, hi;
             f2_split(f2_fma(t[i], inv, f2_fma(m[i], minus1, magic)), lo, hi);   // t * inv less the integer
             worst = max3_abs(worst, lo, hi);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NP; ++i) {
             float lo, hi;
             f2_split(m[i], lo, hi);
             b[2 * i] = __float_as_uint(lo);
@@ -248,7 +249,7 @@ __device__ __forceinline__ void i8_quant8(const uint64_t (&t)[4], const I8RowSca
         }
         if (worst > kI8NearHalf) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NP; ++i) {
                 float lo, hi;
                 f2_split(t[i], lo, hi);
                 b[2 * i] = i8_settle(lo, __uint_as_float(b[2 * i]), s);
@@ -256,6 +257,32 @@ __device__ __forceinline__ void i8_quant8(const uint64_t (&t)[4], const I8RowSca
             }
         }
     }
+}
+
+// Block totals of the warps' maxima and, for a norm, sums (at most 16 warps).
+template <bool NORM>
+__device__ __forceinline__ void i8_block_totals(uint32_t &amax, float &sum, uint32_t *s_max, float *s_sum, int warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) {
+        s_max[warp] = amax;
+        s_sum[warp] = sum;
+    }
+    __syncthreads();
+    amax = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
+    if constexpr (NORM) {
+        sum = lane < warps ? s_sum[lane] : 0.0f;   // lanes 16 .. 31 hold zeros
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+}
+
+// A row's scale as it is stored.
+template <bool NORM>
+__device__ __forceinline__ float i8_stored_scale(uint32_t amax, float sum, bool finite, int C, float eps) {
+    const float A = __uint_as_float(amax);
+    if (!finite) return __uint_as_float(0x7fc00000u);
+    if (amax == 0u) return 0.0f;
+    return NORM ? A * (1.0f / sqrtf(sum / static_cast<float>(C) + eps)) / 127.0f : A / 127.0f;
 }
 
 // One row per group of threads: a block, or a warp (TPR = 32), which takes RW rows at once. A thread
@@ -455,29 +482,11 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }
-        if constexpr (!GROUP_WARP) {
-            if (lane == 0) {
-                s_max[warp] = amax;
-                s_sum[warp] = sum;
-            }
-            __syncthreads();
-            const int warps = tpr >> 5;
-            amax = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
-            if constexpr (NORM) {
-                sum = lane < warps ? s_sum[lane] : 0.0f;   // lanes 16 .. 31 hold zeros
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            }
-        }
+        if constexpr (!GROUP_WARP) i8_block_totals<NORM>(amax, sum, s_max, s_sum, tpr >> 5);
         const bool finite = amax < 0x7f800000u && (!NORM || sum < __uint_as_float(0x7f800000u));
         s[r] = i8_row_scale(amax, finite);
-        if (tid == 0 && row0 + r < p.M) {
-            const float A = __uint_as_float(amax);
-            float sc = NORM ? A * (1.0f / sqrtf(sum / static_cast<float>(C) + p.eps)) / 127.0f : A / 127.0f;
-            if (amax == 0u) sc = 0.0f;
-            if (!finite) sc = __uint_as_float(0x7fc00000u);
-            if (in_bounds(row0 + r, 1, p.M, kSiteI8RowsScale, status)) p.scale[row0 + r] = sc;
-        }
+        if (tid == 0 && row0 + r < p.M && in_bounds(row0 + r, 1, p.M, kSiteI8RowsScale, status))
+            p.scale[row0 + r] = i8_stored_scale<NORM>(amax, sum, finite, C, p.eps);
     }
     for (int c0 = 0; c0 < (STREAM ? C : 1); c0 += piece) {
         if constexpr (STREAM) {
@@ -492,11 +501,161 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
                 for (int i = 0; i < 4; ++i) t[r][k][i] = f2_mul(t[r][k][i], f2_pack(s[r].up, s[r].up));
             }
             uint32_t b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (!s[r].dead) i8_quant8<BF16>(t[r][k], s[r], b);
+            if (!s[r].dead) i8_quant<BF16>(t[r][k], s[r], b);
             store(c0, r, k, b);
         }
         if (C - c0 <= piece) break;
     }
+}
+
+// Rows that start off 16 bytes (odd C, shifted tensors), one per block of TPR threads: bulk copies
+// bring the row's 16-byte interior into shared memory, plain loads its edges, and both passes read
+// it there, an element a lane. The copies in flight take no registers, so many blocks fit on an SM
+// and hide one another's latency (blocks that walk over rows, with the next row's copies ahead, took
+// up to twice as long: a row's work is shorter than a copy's latency).
+template <typename T>
+__host__ __device__ constexpr int i8_staged_bytes(int values) { return (values * static_cast<int>(sizeof(T)) + 31) & ~15; }
+
+template <typename T, int MODE, int TPR>
+__global__ void __launch_bounds__(TPR)
+i8_rows_staged_kernel(const I8RowsParams p, unsigned int *status) {
+    grid_dependents_launch();
+    grid_dependency_wait();
+    constexpr bool NORM = MODE == kI8Norm || MODE == kI8NormResidual, RES = MODE == kI8NormResidual;
+    constexpr bool BF16 = MODE == kI8Plain && sizeof(T) == 2;
+    extern __shared__ __align__(16) uint8_t staged_raw[];
+    __shared__ float s_sum[16];
+    __shared__ uint32_t s_max[16];
+    __shared__ __align__(8) uint64_t s_bar;
+    const int tid = threadIdx.x;
+    const int C = p.C, n_in = MODE == kI8Glu ? 2 * C : C;   // values of x's row
+    const long long row = blockIdx.x, n_elems = p.M * C, x_elems = p.M * n_in;
+    const uint32_t bar = smem_u32(&s_bar);
+
+    // A row's source, and where its values begin in shared memory: as far past 16 bytes as in memory.
+    struct Source {
+        const T *from;
+        T *to;
+        int n, front, inner;   // values; bytes before the first 16-byte boundary, and of whole 16 bytes after it
+    };
+    auto source = [&](bool second) {
+        Source v;
+        v.n = second ? C : n_in;
+        v.from = static_cast<const T *>(second ? p.residual : p.x) + row * v.n;
+        const int off = static_cast<int>(reinterpret_cast<uintptr_t>(v.from) & 15);
+        v.to = reinterpret_cast<T *>(staged_raw + (second ? i8_staged_bytes<T>(C) : 0) + off);
+        v.front = (16 - off) & 15;
+        v.inner = (v.n * static_cast<int>(sizeof(T)) - v.front) & ~15;
+        return v;
+    };
+    const Source sx = source(false), sr = source(RES);
+    T *xs = sx.to, *h = static_cast<T *>(p.h) + row * C;
+    int8_t *q = p.q + row * p.ldq;
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_barrier_init();
+        mbar_arrive_expect_tx(bar, sx.inner + (RES ? sr.inner : 0));
+        const bool in = in_bounds(row * n_in, n_in, x_elems, kSiteI8RowsX, status);
+        auto copy = [&](const Source &v) {
+            if (in) bulk_g2s(smem_u32(v.to) + v.front, reinterpret_cast<const uint8_t *>(v.from) + v.front, v.inner, bar);
+            else mbar_complete_tx(bar, v.inner);
+        };
+        copy(sx);
+        if (RES) copy(sr);
+    }
+    // the edges: the first eight threads have those before the interior, the next eight those after it
+    auto edge = [&](const Source &v) {
+        const int front = v.front / static_cast<int>(sizeof(T)), rest = front + v.inner / static_cast<int>(sizeof(T));
+        const int e = tid < 8 ? tid : rest + tid - 8;
+        if (tid < 16 && (tid < 8 ? e < front : e < v.n) && in_bounds(row * v.n + e, 1, x_elems, kSiteI8RowsX, status))
+            v.to[e] = v.from[e];
+    };
+    edge(sx);
+    if (RES) edge(sr);
+
+    // Four values e, e + TPR, ... of the row (as two pairs) at a time, `all` if they are all in it.
+    constexpr int NP = 2;
+    auto each = [&](auto body) {
+        int e0 = 0;
+        for (; C - e0 >= 2 * NP * TPR; e0 += 2 * NP * TPR) body(e0 + tid, std::true_type());
+        if (e0 < C) body(e0 + tid, std::false_type());
+    };
+    auto weights = [&](int e, auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        return f2_pack(ALL || e < C ? p.weight[e] : 0.0f, ALL || e + TPR < C ? p.weight[e + TPR] : 0.0f);
+    };
+    auto pair = [&](const T *from, int e, auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        return f2_pack(ALL || e < C ? i8_to_float(from[e]) : 0.0f, ALL || e + TPR < C ? i8_to_float(from[e + TPR]) : 0.0f);
+    };
+    __syncthreads();
+    const bool landed = mbar_wait(bar, 0);
+    if (!landed) atomicOr(status, kStatusTimeout);
+
+    uint64_t sum2 = 0;
+    float top = 0.0f;
+    each([&](int e, auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        uint64_t w[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) w[i] = NORM ? weights(e + 2 * i * TPR, all) : 0;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int c = e + 2 * i * TPR;
+            uint64_t t = pair(xs, c, all);
+            if constexpr (MODE == kI8Glu) t = i8_glu(t, pair(xs + C, c, all));
+            if constexpr (RES) {
+                float lo, hi;
+                f2_split(f2_add(t, pair(sr.to, c, all)), lo, hi);
+                const T hlo = i8_type<T>(lo), hhi = i8_type<T>(hi);
+                if (ALL || c < C) h[c] = xs[c] = hlo;
+                if (ALL || c + TPR < C) h[c + TPR] = xs[c + TPR] = hhi;
+                t = f2_pack(i8_to_float(hlo), i8_to_float(hhi));
+            }
+            if constexpr (NORM) {
+                sum2 = f2_fma(t, t, sum2);
+                t = f2_mul(t, w[i]);
+            }
+            float lo, hi;
+            f2_split(t, lo, hi);
+            top = max3_abs(top, lo, hi);
+        }
+    });
+    uint32_t amax = __reduce_max_sync(0xffffffffu, __float_as_uint(top) & 0x7fffffffu);
+    float sum = 0.0f;
+    if constexpr (NORM) {
+        float lo, hi;
+        f2_split(sum2, lo, hi);
+        sum = lo + hi;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    i8_block_totals<NORM>(amax, sum, s_max, s_sum, TPR / 32);
+    const bool finite = amax < 0x7f800000u && (!NORM || sum < __uint_as_float(0x7f800000u));
+    const I8RowScale s = i8_row_scale(amax, finite);
+    if (tid == 0 && in_bounds(row, 1, p.M, kSiteI8RowsScale, status))
+        p.scale[row] = i8_stored_scale<NORM>(amax, sum, finite, C, p.eps);
+    each([&](int e, auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        uint64_t t[NP], w[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) w[i] = NORM ? weights(e + 2 * i * TPR, all) : 0;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int c = e + 2 * i * TPR;
+            t[i] = pair(xs, c, all);
+            if constexpr (MODE == kI8Glu) t[i] = i8_glu(t[i], pair(xs + C, c, all));
+            if constexpr (NORM) t[i] = f2_mul(t[i], w[i]);
+            if (s.up != 1.0f) t[i] = f2_mul(t[i], f2_pack(s.up, s.up));
+        }
+        uint32_t b[2 * NP] = {};
+        if (!s.dead) i8_quant<BF16>(t, s, b);
+#pragma unroll
+        for (int i = 0; i < 2 * NP; ++i)
+            if ((ALL || e + i * TPR < C) && in_bounds(row * C + e + i * TPR, 1, n_elems, kSiteI8RowsQ, status))
+                q[e + i * TPR] = static_cast<int8_t>(b[i]);
+    });
+    if (!landed) mbar_wait(bar, 0);   // no copy of this block is in flight when it ends
 }
 
 }  // namespace convb200

@@ -277,8 +277,8 @@ int dwpw_fwd(const float *x, const float *w_dw, const float *b_dw, const void *F
  * pointer off the 16-byte rule CONV_ERR_MISALIGNED; other pointers are aligned to their element
  * (16-byte aligned tensors are faster). There are no atomics: the sum of squares of a norm has an
  * order that C and the pointers' alignment fix, every other result does not depend on the launch.
- * conv_last_kernel() afterwards names i8_rows_kernel, i8_filter_kernel, i8_dequant_kernel,
- * i8_split_kernel (few tokens) or i8_pair_kernel.
+ * conv_last_kernel() afterwards names i8_rows_kernel, i8_rows_staged_kernel (rows off 16 bytes),
+ * i8_filter_kernel, i8_dequant_kernel, i8_split_kernel (few tokens) or i8_pair_kernel.
  */
 typedef enum {
     CONV_BF16 = 0,

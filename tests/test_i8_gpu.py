@@ -54,7 +54,8 @@ def _close(a, b, rel):
 # widths on both sides of every kernel's limit: a warp a row (512, 1024), a block (8192, 16384), pieces
 # above; multiples of 8 and odd ones
 WIDTHS = [(1, 1), (2, 8), (3, 7), (5, 64), (2, 127), (33, 512), (9, 520), (2, 1001), (4, 1024), (3, 1025), (3, 1032),
-          (2, 2056), (7, 4096), (2, 5003), (1, 8192), (2, 8200), (2, 12343), (3, 16384), (2, 16385), (1, 20000), (2, 40001)]
+          (2, 2056), (2, 2049), (2, 4001), (7, 4096), (2, 5003), (1, 8192), (2, 8200), (2, 9224), (2, 10240), (2, 10248), (2, 12343),
+          (3, 16384), (2, 16385), (1, 20000), (2, 40001), (1, 57001), (1, 113001)]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
@@ -384,6 +385,25 @@ def test_tensors_off_16_bytes(cb, M, C, dtype):
             assert torch.equal(cb.pointwise_i8_fwd(q, scale, wq, ws, y=y), cb.pointwise_i8_fwd(q, scale, wq, ws, dtype=dtype))
         finally:
             del os.environ["CONV_B200_I8"]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("C", [3000, 9001, 17000])
+def test_norm_of_tensors_that_start_apart(cb, C, dtype):
+    """x, the residual and h each off 16 bytes by a different number of elements; then in place."""
+    g, M = _gen(C, 6), 3
+
+    def view(off):
+        return _normal(g, M * C + off, dtype=dtype)[off:].view(M, C)
+    x, r, w = view(1), view(3), 1 + 0.1 * _normal(g, C)
+    rq, rs, rh = ref.rmsnorm(x, w, r)
+    for h in (view(2), r, x):
+        a, b = (x.clone(), r.clone()) if h is x or h is r else (x, r)
+        q, scale, h = cb.rmsnorm_i8_fwd(x, w, r, h=h)
+        assert torch.equal(h.cpu(), rh) and np.array_equal(_q(q), rq)
+        _close(scale.cpu().numpy(), rs, ((64 * (C // 16384 + 1) + 10) / 2 + 5) * U)
+        x.copy_(a)
+        r.copy_(b)
 
 
 def test_gates_far_from_zero(cb):
