@@ -73,7 +73,7 @@ int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
         return launch_i8_rows<T, MODE, 4, true, 0, 1, true>(p, 512, stream, d);
     }
     // Element by element: in registers up to 2048 values (8192 x 901: 16.4 us with 128 threads a row, 11.4
-    // with a warp), in float32 up to 8192 (1031 x 5003 10.1 us, staged 10.6; with a residual 15.4 and 17.0;
+    // with a warp), in float32 up to 8192 (1031 x 5003 with a norm 8.5 us, staged 10.6; with a residual 14.5 and 17.0;
     // two inputs at four groups a thread would take too many registers); beyond that staged (bf16: 8192 x
     // 4095 30.4 us in registers, 20.3 staged; 4096 x 12343 77.6 streamed, 28.0 staged), in float32 while two
     // blocks fit on an SM (1024 x 17001 27.6 us streamed, 17.2 staged; 1024 x 30001 38.2 and 41.3), in bf16
@@ -83,6 +83,10 @@ int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
     if (C <= 2048) return launch_i8_rows<T, MODE, 2, false, 128, 1, false>(p, 128, stream, d);
     if constexpr (sizeof(T) == 4) {
         if (C <= 4096) return launch_i8_rows<T, MODE, 2, false, 256, 1, false>(p, 256, stream, d);
+        if (C <= 6144) {   // 4096 x 5003 with a norm: 30.1 us in the slots of 8192, 23.4 in those of 6144
+            if constexpr (MODE == kI8Plain || MODE == kI8Norm) return launch_i8_rows<T, MODE, 3, false, 256, 1, false>(p, 256, stream, d);
+            else return launch_i8_rows<T, MODE, 2, false, 384, 1, false>(p, 384, stream, d);
+        }
         if (C <= 8192) {
             if constexpr (MODE == kI8Plain || MODE == kI8Norm) return launch_i8_rows<T, MODE, 4, false, 256, 1, false>(p, 256, stream, d);
             else return launch_i8_rows<T, MODE, 2, false, 512, 1, false>(p, 512, stream, d);

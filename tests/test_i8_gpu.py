@@ -54,7 +54,7 @@ def _close(a, b, rel):
 # widths on both sides of every kernel's limit: a warp a row (512, 1024), a block (8192, 16384), pieces
 # above; multiples of 8 and odd ones
 WIDTHS = [(1, 1), (2, 8), (3, 7), (5, 64), (2, 127), (33, 512), (9, 520), (2, 1001), (4, 1024), (3, 1025), (3, 1032),
-          (2, 2056), (2, 2049), (2, 4001), (7, 4096), (2, 5003), (1, 8192), (2, 8200), (2, 9224), (2, 10240), (2, 10248), (2, 12343),
+          (2, 2056), (2, 2049), (2, 4001), (7, 4096), (2, 5003), (2, 6145), (2, 8191), (1, 8192), (2, 8200), (2, 9224), (2, 10240), (2, 10248), (2, 12343),
           (3, 16384), (2, 16385), (1, 20000), (2, 40001), (1, 57001), (1, 113001)]
 
 
