@@ -61,7 +61,9 @@ __device__ __forceinline__ void i8_out(__nv_bfloat16 *p, float v) { *p = __float
 // that leaves room for a second CTA -- of the same launch where there are more CTAs than SMs, or of
 // the next one, which then sets up, and asks L2 for its first k blocks of the filter, while this one
 // finishes (1 x 4096 x 4096 split in 4, filters in HBM: 6.0 us with the long ring, 5.7 with the
-// short one, 5.2 with the request).
+// short one, 5.2 with the request). The long ring of 16 columns asks too (1 x 4096 x 16384: 13.4 us
+// without, 12.65 with); wider tiles do not, since behind a kernel that fills the SMs they ask when
+// they could load (128 x 4096 x 4096: 7.9 and 8.9 us).
 template <int BN_, int STAGES_, int KB_>
 struct I8SplitCfg {
     static constexpr int BN = BN_, STAGES = STAGES_, KB = KB_;
@@ -125,10 +127,17 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
     const uint32_t tmem_base = *tmem_holder;
     // the peers' shared memory may be written once they have arrived here
     if (S > 1) cluster_arrive();
-    if constexpr (KB == 1 && BN <= 32) {
-        if (warp == 0) {
+    if constexpr (BN == 16 || (BN == 32 && KB == 1)) {
+        if (warp == 2) {
             const uint32_t leader = elect_one_sync();
-            for (int sb = sb0; sb < sb1 && sb < sb0 + 8; ++sb) tma_prefetch_2d_if(&tmW, sb * 128, n0, leader);
+            for (int sb = sb0; sb < sb1 && sb < sb0 + 8; ++sb) {
+                if (KB > 1 && p.wide) {
+                    tma_prefetch_3d_if(&tmW, 0, n0, sb * KB, leader);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) tma_prefetch_2d_if(&tmW, (sb * KB + b) * 128, n0, leader);
+                }
+            }
         }
     }
     grid_dependency_wait();
@@ -272,6 +281,9 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 // of the accumulator. Two accumulators, so tile t + 1 multiplies while tile t is scaled and stored.
 //   warp 0      TMA ring of STAGES slots
 //   warp 1      TMEM allocation; the even CTA's issues the MMAs for both
+//   warp 2      first asks L2 for the filter's first blocks, which a launch behind the kernel that
+//               quantises its rows does while that one runs (512 x 4096 x 4096 with the norm: 16.7
+//               us without, 16.3 with; behind another product it makes no difference)
 //   warps 2..17 epilogue, four warps per TMEM lane quarter with a quarter of the columns each, in
 //               units of 64 bytes of output a row: tcgen05.ld, scale, round, swizzled staging, one
 //               tensor store a unit. A warp has its columns' scales and biases fetched a tile ahead
@@ -358,6 +370,13 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     cluster_sync_all();   // both CTAs' barriers and TMEM exist before either is used
     tc_fence_after();
     const uint32_t tmem_base = *tmem_holder;
+    if (warp == 2 && static_cast<int>(blockIdx.x >> 1) < p.num_tiles) {   // its first filter blocks into L2
+        const uint32_t leader = elect_one_sync();
+        int mt, nt;
+        i8_tile(static_cast<int>(blockIdx.x >> 1), p.m_tiles, p.n_tiles, mt, nt);
+        for (int kb = 0; kb < p.num_kblk && kb < 8; ++kb)
+            tma_prefetch_2d_if(&tmW, kb * 128, nt * Cfg::BN + static_cast<int>(rank) * (Cfg::BN / 2), leader);
+    }
     grid_dependency_wait();
 
     auto fail = [&]() {

@@ -58,6 +58,15 @@ __device__ __forceinline__ void tma_prefetch_2d_if(const CUtensorMap *m, int x, 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_3d_if(const CUtensorMap *m, int x, int y, int z, uint32_t leader) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n\t}"
+        :
+        : "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(leader)
+        : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d_if(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x, int y, int z,
                                                uint32_t leader) {
     asm volatile(
