@@ -216,15 +216,21 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
                 }
             }
             if (!plain || (!BF16 && worst > kI8NearHalf)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
 #pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t settled = i8_quant1(i8_to_float(slab[(g * 4 + j) * kI8FilterCols + cg + i]), sc[i]);
+                for (int j = 0; j < 4; ++j) {   // a row's four values at once: a warp here holds up its CTA
+                    uint64_t t[2];
+                    four(g * 4 + j, t[0], t[1]);
+                    float v[4];
+                    f2_split(t[0], v[0], v[1]);
+                    f2_split(t[1], v[2], v[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t settled = i8_quant1(v[i], sc[i]);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (k == j) m[k][i] = settled;
                     }
+                }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -179,7 +179,7 @@ __device__ __forceinline__ I8RowScale i8_row_scale(uint32_t amax_bits, bool fini
 }
 
 constexpr float kI8Magic = 12582912.0f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
-constexpr float kI8NearHalf = 0.49996f;   // 4e-5 off a half: v * inv is off by at most 127 * 2^-24 < 8e-6
+constexpr float kI8NearHalf = 0.49999f;   // 1e-5 off a half: v * inv is off by at most 127 * 2^-24 < 7.6e-6
 constexpr float kI8Below = 1.0f - 0x1p-20f, kI8Above = 1.0f + 0x1p-20f;
 
 // The integer m = kI8Magic + k, k the nearest to v * inv, made the nearest to 127 v / A. With `side`
