@@ -39,6 +39,7 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ uint32_t s_part[8][kI8FilterCols];
     __shared__ uint32_t s_max[kI8FilterCols];        // this CTA's maxima, read by the cluster
+    __shared__ __align__(16) float s_scale[3][kI8FilterCols];   // of the columns: A, inv and up (I8RowScale), inv 0 if dead
     constexpr int ROW = kI8FilterCols * sizeof(T);   // bytes of a staged row
     constexpr int CHUNKS = ROW / 16;
     T *slab = reinterpret_cast<T *>(dyn);                    // [piece][32]
@@ -162,20 +163,25 @@ i8_filter_kernel(const I8FilterParams p, unsigned int *status) {
             asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_rank(smem_u32(&s_max[threadIdx.x]), r < S ? r : 0u)));
             m = max(m, v);
         }
-        s_part[0][threadIdx.x] = m;
+        const bool finite = m < 0x7f800000u;
+        const I8RowScale c = i8_row_scale(m, finite);
+        s_scale[0][threadIdx.x] = c.A;
+        s_scale[1][threadIdx.x] = c.inv;
+        s_scale[2][threadIdx.x] = c.up;
+        const int o = o0 + static_cast<int>(threadIdx.x);
+        if (rank == 0 && o < p.Cout && in_bounds(o, 1, p.Cout, kSiteI8FilterScale, status))
+            p.scale[o] = finite ? __uint_as_float(m) / 127.0f : __uint_as_float(0x7fc00000u);
     }
     __syncthreads();
     I8RowScale sc[4];
     bool plain = true;   // no column of zeros, tiny, huge or not finite
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t m = s_part[0][cg + i];
-        const bool finite = m < 0x7f800000u;
-        sc[i] = i8_row_scale(m, finite);
+        sc[i].A = s_scale[0][cg + i];
+        sc[i].inv = s_scale[1][cg + i];
+        sc[i].up = s_scale[2][cg + i];
+        sc[i].dead = sc[i].inv == 0.0f;
         plain = plain && !sc[i].dead && sc[i].up == 1.0f;
-        const int o = o0 + cg + i;
-        if (rank == 0 && threadIdx.x < 8 && o < p.Cout && in_bounds(o, 1, p.Cout, kSiteI8FilterScale, status))
-            p.scale[o] = finite ? __uint_as_float(m) / 127.0f : __uint_as_float(0x7fc00000u);
     }
     cluster_arrive();   // these maxima have been read; nobody leaves before all have (cluster_wait below)
 
