@@ -95,7 +95,8 @@ int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
     const long long bytes = 1LL * i8_staged_bytes<T>(MODE == kI8Glu ? 2 * C : C) * (MODE == kI8NormResidual ? 2 : 1);
     if (bytes <= (sizeof(T) == 4 ? kI8StagedMax / 2 : kI8StagedMax)) {
         const int n = static_cast<int>(bytes);
-        if (C <= 4096) return launch_i8_staged<T, MODE, 128>(p, n, stream, d);
+        if constexpr (sizeof(T) == 2)
+            if (C <= 4096) return launch_i8_staged<T, MODE, 128>(p, n, stream, d);
         if (C <= 16384) return launch_i8_staged<T, MODE, 256>(p, n, stream, d);
         return launch_i8_staged<T, MODE, 512>(p, n, stream, d);
     }
