@@ -143,6 +143,21 @@ def _device(*tensors):
     return devs.pop()
 
 
+def _empty_on(stream, shape, dtype, device):
+    """Uninitialised memory that a call on `stream` (the device's current one when None) uses: from the
+    allocator's blocks of that stream, as under torch.cuda.stream(stream). A block of another stream
+    could still be in use there when this call writes it, and a workspace dropped at return could
+    be handed out there while this call's kernels run."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle = _stream(stream, device).value or 0
+    if not isinstance(stream, torch.cuda.Stream):   # a handle; 0 and 1 are the default stream
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle > 1 else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(fn, what, tensors, stream, *args):
     """Runs one C entry point with the tensors' device current (the library launches on the
     current device) and its stream as the last argument."""
@@ -179,7 +194,7 @@ def _dense(X, F, Y, stream, dtype, fn, what):
     if K > min(H, W):
         raise ValueError("K must not exceed min(H, W)")
     if Y is None:
-        Y = torch.empty((N, H - K + 1, W - K + 1, Cout), dtype=dtype, device=X.device)
+        Y = _empty_on(stream, (N, H - K + 1, W - K + 1, Cout), dtype, X.device)
     elif tuple(Y.shape) != (N, H - K + 1, W - K + 1, Cout):
         raise ValueError("Y has the wrong shape")
     py = _tensor(Y, dtype, 4, "Y")
@@ -219,7 +234,7 @@ def conv2d_nhwc_fwd_ex(X, F, bias=None, Y=None, stride=1, pad=0, dil=1, stream=N
     if Ho < 1 or Wo < 1:
         raise ValueError("empty output")
     if Y is None:
-        Y = torch.empty((N, Ho, Wo, Cout), dtype=torch.bfloat16, device=X.device)
+        Y = _empty_on(stream, (N, Ho, Wo, Cout), torch.bfloat16, X.device)
     elif tuple(Y.shape) != (N, Ho, Wo, Cout):
         raise ValueError("Y has the wrong shape")
     py = _tensor(Y, torch.bfloat16, 4, "Y")
@@ -279,7 +294,7 @@ def conv2d_nhwc_fwd_grouped(X, F, bias=None, Y=None, stride=1, pad=0, dil=1, gro
     if Ho < 1 or Wo < 1:
         raise ValueError("empty output")
     if Y is None:
-        Y = torch.empty((N, Ho, Wo, Cout), dtype=torch.bfloat16, device=X.device)
+        Y = _empty_on(stream, (N, Ho, Wo, Cout), torch.bfloat16, X.device)
     elif tuple(Y.shape) != (N, Ho, Wo, Cout):
         raise ValueError("Y has the wrong shape")
     py = _tensor(Y, torch.bfloat16, 4, "Y")
@@ -306,11 +321,11 @@ def conv2d_nhwc_fwd_im2col(X, F, Y=None, workspace=None, stream=None):
     if need == 0:
         raise ValueError("invalid shape")
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = _empty_on(stream, need, torch.uint8, X.device)
     if not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if Y is None:
-        Y = torch.empty((N, H - K + 1, W - K + 1, Cout), dtype=torch.bfloat16, device=X.device)
+        Y = _empty_on(stream, (N, H - K + 1, W - K + 1, Cout), torch.bfloat16, X.device)
     py = _tensor(Y, torch.bfloat16, 4, "Y")
     _call(lib.conv2d_nhwc_fwd_im2col, "conv2d_nhwc_fwd_im2col", (X, F, Y, workspace), stream,
           px, pf, py, ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(),
@@ -359,7 +374,7 @@ def depthwise_fwd(x, w, bias=None, y=None, stride=1, pad=0, dil=1, mode=DW_EXACT
     if Ho < 1 or Wo < 1:
         raise ValueError("empty output")
     if y is None:
-        y = torch.empty((N, Cout, Ho, Wo), dtype=torch.float32, device=x.device)
+        y = _empty_on(stream, (N, Cout, Ho, Wo), torch.float32, x.device)
     elif tuple(y.shape) != (N, Cout, Ho, Wo):
         raise ValueError("y has the wrong shape")
     py = _tensor(y, torch.float32, 4, "y")
@@ -397,7 +412,7 @@ def dwpw_fwd(x, w_dw, b_dw, F, b_pw=None, y=None, stride=1, pad=0, dil=1, mode=D
     if Ho < 1 or Wo < 1:
         raise ValueError("empty output")
     if y is None:
-        y = torch.empty((N, Cout, Ho, Wo), dtype=torch.float32, device=x.device)
+        y = _empty_on(stream, (N, Cout, Ho, Wo), torch.float32, x.device)
     elif tuple(y.shape) != (N, Cout, Ho, Wo):
         raise ValueError("y has the wrong shape")
     py = _tensor(y, torch.float32, 4, "y")
@@ -502,32 +517,34 @@ def empty_rows_i8(rows, C, device="cuda"):
     """An uninitialised int8 matrix [rows, C] in the layout the 8-bit operators take, a view of
     [rows, pitch] whose rows start where conv_i8_row_pitch puts them. Copy 8-bit rows from
     elsewhere (a checkpoint's filter) into one with copy_()."""
+    return _i8_empty_rows(rows, C, device, None)
+
+
+def _i8_empty_rows(rows, C, device, stream):
     import torch
     _i8_sizes("the matrix", int(rows), int(C))
     pitch = lib.conv_i8_row_pitch(int(C))
     if pitch == 0 or rows < 1:
         raise ValueError("rows and C must be positive")
-    return torch.empty((rows, pitch), dtype=torch.int8, device=device)[:, :C]
+    return _empty_on(stream, (rows, pitch), torch.int8, device)[:, :C]
 
 
-def _i8_out(q, scale, rows, C, device):
+def _i8_out(q, scale, rows, C, device, stream):
     """q and scale (allocated where None), their addresses and q's pitch."""
-    import torch
     if q is None:
-        q = empty_rows_i8(rows, C, device)
+        q = _i8_empty_rows(rows, C, device, stream)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=device)
+        scale = _empty_on(stream, rows, _F32, device)
     pq, n, c, pitch = _i8_rows(q, "q")
     if n != rows or c != C:
         raise ValueError(f"q must have shape {(rows, C)}, got {(n, c)}")
     return q, scale, pq, pitch, _i8_ptr(scale, _F32, (rows,), "scale")
 
 
-def _i8_result(y, dtype, shape, device):
+def _i8_result(y, dtype, shape, device, stream):
     """y (allocated where None), its conv_dtype and its address."""
     if y is None:
-        import torch
-        y = torch.empty(shape, dtype=torch.bfloat16 if dtype is None else dtype, device=device)
+        y = _empty_on(stream, shape, _BF16 if dtype is None else dtype, device)
     elif dtype is not None and y.dtype is not dtype:
         raise TypeError(f"y must be {dtype}, got {y.dtype}")
     if y.dtype is _BF16:
@@ -559,12 +576,11 @@ def rmsnorm_i8_fwd(x, weight, residual=None, h=None, q=None, scale=None, eps=1e-
     if residual is not None:
         pr = _i8_ptr(residual, x.dtype, shape, "residual")
         if h is None:
-            import torch
-            h = torch.empty_like(x)
+            h = _empty_on(stream, shape, x.dtype, x.device)
         ph = _i8_ptr(h, x.dtype, shape, "h")
     elif h is not None:
         raise ValueError("h is x + residual: give the residual too")
-    q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
+    q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device, stream)
     _call(lib.rmsnorm_i8_fwd, "rmsnorm_i8_fwd", (residual, weight, h, q, scale, x), stream,
              px, pr, pw, ph, pq, ps, M, C, ldq, float(eps), dt)
     return q, scale, h
@@ -587,7 +603,7 @@ def quant_rows_i8_fwd(x, glu=False, q=None, scale=None, stream=None):
         if C % 2:
             raise ValueError("glu needs x [M, 2C]")
         C //= 2
-    q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device)
+    q, scale, pq, ldq, ps = _i8_out(q, scale, M, C, x.device, stream)
     _call(lib.quant_rows_i8_fwd, "quant_rows_i8_fwd", (q, scale, x), stream,
              px, pq, ps, M, C, ldq, 1 if glu else 0, dt)
     return q, scale
@@ -609,7 +625,7 @@ def quant_filter_i8_fwd(F, q=None, scale=None, stream=None):
             return oq, os
     dt, pf = _i8_matrix(F, "F")
     Cin, Cout = F.shape
-    q, scale, pq, ldw, ps = _i8_out(q, scale, Cout, Cin, F.device)
+    q, scale, pq, ldw, ps = _i8_out(q, scale, Cout, Cin, F.device, stream)
     _call(lib.quant_filter_i8_fwd, "quant_filter_i8_fwd", (q, scale, F), stream,
              pf, pq, ps, Cin, Cout, ldw, dt)
     return q, scale
@@ -625,7 +641,7 @@ def dequant_rows_i8_fwd(q, scale, y=None, dtype=None, stream=None):
             return out
     pq, M, C, ldq = _i8_rows(q, "q")
     ps = _i8_ptr(scale, _F32, (M,), "scale")
-    y, dt, py = _i8_result(y, dtype, (M, C), q.device)
+    y, dt, py = _i8_result(y, dtype, (M, C), q.device, stream)
     _call(lib.dequant_rows_i8_fwd, "dequant_rows_i8_fwd", (scale, y, q), stream,
              pq, ps, py, M, C, ldq, dt)
     return y
@@ -646,7 +662,7 @@ def pointwise_i8_fwd(q, q_scale, Wq, w_scale, bias=None, y=None, dtype=None, str
         raise ValueError(f"Wq must have q's {Cin} columns, got {Cin2}")
     ps, pws = _i8_ptr(q_scale, _F32, (M,), "q_scale"), _i8_ptr(w_scale, _F32, (Cout,), "w_scale")
     pb = None if bias is None else _i8_ptr(bias, _F32, (Cout,), "bias")
-    y, dt, py = _i8_result(y, dtype, (M, Cout), q.device)
+    y, dt, py = _i8_result(y, dtype, (M, Cout), q.device, stream)
     _call(lib.pointwise_i8_fwd, "pointwise_i8_fwd", (q_scale, Wq, w_scale, bias, y, q), stream,
              pq, ps, pw, pws, pb, py, M, Cin, Cout, ldq, ldw, dt)
     return y
@@ -674,11 +690,11 @@ def conv2d_nhwc_fwd_i8(X, Wq, w_scale, bias=None, norm=None, eps=1e-6, Y=None, w
         need = lib.conv2d_nhwc_i8_workspace(N, H, W, Cin)
         if need == 0:
             raise ValueError("invalid shape")
-        workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+        workspace = _empty_on(stream, need, torch.uint8, X.device)
     elif not (workspace.is_cuda and workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if Y is None:
-        Y = torch.empty((N, H, W, Cout), dtype=torch.bfloat16, device=X.device)
+        Y = _empty_on(stream, (N, H, W, Cout), torch.bfloat16, X.device)
     py = _i8_ptr(Y, _BF16, (N, H, W, Cout), "Y")
     _call(lib.conv2d_nhwc_fwd_i8, "conv2d_nhwc_fwd_i8", (norm, Wq, w_scale, bias, Y, workspace, X), stream,
              px, pn, float(eps), pw, pws, pb, py, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
