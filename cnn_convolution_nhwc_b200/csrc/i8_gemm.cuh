@@ -55,15 +55,21 @@ __device__ __forceinline__ void i8_out(__nv_bfloat16 *p, float v) { *p = __float
 //               issuing warp 0.08 us whatever its size, so a slot of two k blocks is two copies of
 //               3-D boxes (128 values, rows, k blocks) where Cin is a multiple of 128; elsewhere
 //               a k block each, whose extent ends at Cin (p.wide).
-//   warp 1      TMEM allocation, MMA issue (M = 128, N = BN)
+//   warp 1      TMEM allocation, MMA issue (M = 128, N = BN). TMEM is taken after the dependency wait: a
+//               CTA that held columns while it waited could keep a predecessor's CTA on the same SM,
+//               which takes its own only once it runs, waiting for good. The first copies, which
+//               warp 0 issues meanwhile, hide it
 //   warps 2..9  epilogue, two warps per TMEM lane quarter taking alternate groups of 16 tokens
 // Two forms: a ring that fills an SM's shared memory, for long shares of k, and a short one (KB = 1)
 // that leaves room for a second CTA -- of the same launch where there are more CTAs than SMs, or of
 // the next one, which then sets up, and asks L2 for its first k blocks of the filter, while this one
-// finishes (1 x 4096 x 4096 split in 4, filters in HBM: 6.0 us with the long ring, 5.7 with the
-// short one, 5.2 with the request). The long ring of 16 columns asks too (1 x 4096 x 16384: 13.4 us
-// without, 12.65 with); wider tiles do not, since behind a kernel that fills the SMs they ask when
-// they could load (128 x 4096 x 4096: 7.9 and 8.9 us).
+// finishes (1 x 4096 x 4096 split in 4, filters in HBM: 5.7 us without the request, 5.4 with three
+// blocks, 5.5 with four; with eight, which then compete with this launch's copies, 6.0). The next
+// launch is let in after the dependency wait, not before it, so that it is the next one that sets up
+// early and not the one after it (16 x 2048 x 2048 with its rows: 5.6 and 5.3 us; 1 x 1024 x 1024:
+// 3.05 and 2.85). The long ring of 16 columns asks too (1 x 4096 x 16384: 13.2 us without, 12.8
+// with); wider tiles do not, since behind a kernel that fills the SMs they ask when they could load
+// (128 x 4096 x 4096: 7.9 and 8.9 us).
 template <int BN_, int STAGES_, int KB_>
 struct I8SplitCfg {
     static constexpr int BN = BN_, STAGES = STAGES_, KB = KB_;
@@ -81,7 +87,6 @@ template <class Cfg, typename OUT>
 __global__ void __launch_bounds__(Cfg::THREADS)
 i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmQ, const I8GemmParams p,
                 unsigned int *status) {
-    grid_dependents_launch();
     constexpr int BN = Cfg::BN, STAGES = Cfg::STAGES, KB = Cfg::KB;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
@@ -117,20 +122,13 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmQ);
     }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_holder), Cfg::TMEM_COLS);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem_base = *tmem_holder;
     // the peers' shared memory may be written once they have arrived here
     if (S > 1) cluster_arrive();
     if constexpr (BN == 16 || (BN == 32 && KB == 1)) {
         if (warp == 2) {
             const uint32_t leader = elect_one_sync();
-            for (int sb = sb0; sb < sb1 && sb < sb0 + 8; ++sb) {
+            for (int sb = sb0; sb < sb1 && sb < sb0 + (KB > 1 ? 8 : 3); ++sb) {
                 if (KB > 1 && p.wide) {
                     tma_prefetch_3d_if(&tmW, 0, n0, sb * KB, leader);
                 } else {
@@ -141,6 +139,7 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         }
     }
     grid_dependency_wait();
+    grid_dependents_launch();
 
     if (warp == 0) {
         const uint32_t leader = elect_one_sync();
@@ -172,6 +171,10 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
                 break;
             }
     } else if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_holder), Cfg::TMEM_COLS);
+        tmem_relinquish();
+        __syncwarp();
+        const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_holder);
         const uint32_t leader = elect_one_sync();
         bool ok = true;
         uint32_t s = 0, ph = 0;
@@ -198,8 +201,9 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
         if (!mbar_wait_warp(accf, 0) && lane == 0) { atomicOr(status, kStatusTimeout); *abort_flag = 1; }
     }
     tc_fence_before();
-    __syncthreads();   // also publishes s_scale
+    __syncthreads();   // also publishes s_scale and where TMEM starts
     tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
 
     const int quarter = warp & 3;            // TMEM lanes of this warp (warps 2..9)
     const int eg = (warp - 2) >> 2;          // which of the quarter's two warps
@@ -280,10 +284,11 @@ i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__
 // stages 128 token rows and BN / 2 filter rows per k block and receives its 128 tokens x BN columns
 // of the accumulator. Two accumulators, so tile t + 1 multiplies while tile t is scaled and stored.
 //   warp 0      TMA ring of STAGES slots
-//   warp 1      TMEM allocation; the even CTA's issues the MMAs for both
-//   warp 2      first asks L2 for the filter's first blocks, which a launch behind the kernel that
-//               quantises its rows does while that one runs (512 x 4096 x 4096 with the norm: 16.7
-//               us without, 16.3 with; behind another product it makes no difference)
+//   warp 1      TMEM allocation (after the dependency wait, as in the split kernel, while warp 0 issues
+//               the first copies); the even CTA's issues the MMAs for both
+//   warp 2      first asks L2 for the filter's first four blocks, which a launch behind the kernel
+//               that quantises its rows does while that one runs (512 x 4096 x 4096 with the norm: 16.8
+//               us without, 16.5 with; behind another product 11.3 and 11.2, and 11.4 with eight)
 //   warps 2..17 epilogue, four warps per TMEM lane quarter with a quarter of the columns each, in
 //               units of 64 bytes of output a row: tcgen05.ld, scale, round, swizzled staging, one
 //               tensor store a unit. A warp has its columns' scales and biases fetched a tile ahead
@@ -361,23 +366,31 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         prefetch_tensormap(&tmW);
         if (p.vec) prefetch_tensormap(&tmY);
     }
-    if (warp == 1) {
-        tmem_alloc_pair(smem_u32(tmem_holder), 2 * Cfg::BN);
-        tmem_relinquish_pair();
-    }
-    tc_fence_before();
     __syncthreads();
-    cluster_sync_all();   // both CTAs' barriers and TMEM exist before either is used
-    tc_fence_after();
-    const uint32_t tmem_base = *tmem_holder;
+    cluster_sync_all();   // both CTAs' barriers exist before either is used
+    // Both CTAs' TMEM exists before either is used: warp 1 arrives once it has it, the others here, and
+    // those that use TMEM wait for that (warp 0 after its copies).
+    if (warp != 1) cluster_arrive();
     if (warp == 2 && static_cast<int>(blockIdx.x >> 1) < p.num_tiles) {   // its first filter blocks into L2
         const uint32_t leader = elect_one_sync();
         int mt, nt;
         i8_tile(static_cast<int>(blockIdx.x >> 1), p.m_tiles, p.n_tiles, mt, nt);
-        for (int kb = 0; kb < p.num_kblk && kb < 8; ++kb)
+        for (int kb = 0; kb < p.num_kblk && kb < 4; ++kb)
             tma_prefetch_2d_if(&tmW, kb * 128, nt * Cfg::BN + static_cast<int>(rank) * (Cfg::BN / 2), leader);
     }
     grid_dependency_wait();
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_holder), 2 * Cfg::BN);
+        tmem_relinquish_pair();
+        tc_fence_before();
+        cluster_arrive();
+    }
+    auto tmem_ready = [&]() {
+        cluster_wait();
+        tc_fence_after();
+        return *reinterpret_cast<volatile uint32_t *>(tmem_holder);
+    };
+    uint32_t tmem_base = 0;
 
     auto fail = [&]() {
         atomicOr(status, kStatusTimeout);
@@ -407,7 +420,10 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         // drain: every copy issued has been consumed (the even CTA's commits report to both)
         for (uint32_t j = it > (uint32_t)Cfg::STAGES ? it - Cfg::STAGES : 0u; j < it; ++j)
             if (!mbar_wait_warp(empty(j % Cfg::STAGES), (j / Cfg::STAGES) & 1u)) { if (lane == 0) fail(); break; }
+        __syncwarp();
+        cluster_wait();
     } else if (warp == 1) {
+        tmem_base = tmem_ready();
         const uint32_t leader = elect_one_sync();
         constexpr uint16_t kBoth = 0x3;
         if (rank == 0) {
@@ -468,6 +484,7 @@ i8_pair_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
         };
         if (first < p.num_tiles) fetch(first);
+        tmem_base = tmem_ready();
         uint32_t local = 0;
         for (int t = first; t < p.num_tiles; t += step, ++local) {
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
