@@ -421,6 +421,14 @@ int launch_dense_tc(const void *X, const void *F, void *Y, int N, int H, int W, 
 
 // ---- halo kernel ------------------------------------------------------------------------
 constexpr int kSmemLimit = 232448;   // 227 KB of dynamic shared memory per CTA
+// Kernels of two streams may meet on an SM. Two CTAs that together want more than TMEM's 512 columns
+// are no danger while one of them ends by itself; but if each belongs to a cluster and waits for a
+// CTA that the other kernel keeps waiting elsewhere, neither ends. The smallest cluster kernel with
+// TMEM is the 8-bit product's short split form; a cluster kernel with 512 columns takes more
+// shared memory than that leaves of an SM's 228 KB (1 KB of them reserved per CTA).
+constexpr int kClusterAloneSmem = 228 * 1024 - 2 * 1024 - I8ShortSplit32::SMEM + 1;
+static_assert(I8ShortSplit32::SMEM <= I8ShortSplit16::SMEM, "the smaller of the two short forms");
+static_assert(I8PairCfg<256, 5>::SMEM >= kClusterAloneSmem, "the 8-bit pair kernel beside the short split form");
 
 struct HaloPlan {
     bool ok = false;
@@ -500,7 +508,7 @@ HaloPlan plan_halo(int N, int H, int W, int Cin, int Cout, int K, int num_sms, i
         pl.grid = p.num_tiles < num_sms ? p.num_tiles : num_sms;
     }
     pl.smem = fixed + p.b_region + p.HS * halo_bytes;
-    // more than half of the shared memory keeps a second CTA (and its TMEM allocation) off the SM
+    // more than half of the shared memory keeps a second CTA like this one (and its TMEM allocation) off the SM
     if (pl.smem < 116 * 1024) pl.smem = 116 * 1024;
     pl.bn = bn;
     pl.ok = pl.smem <= kSmemLimit && pl.grid >= 1;
@@ -599,7 +607,7 @@ FoldPlan plan_fold(int N, int H, int W, int Cin, int Cout, int K, int num_sms) {
     p.div_h = make_fastdiv(static_cast<uint32_t>(H));
     pl.grid = p.num_tiles < num_sms ? p.num_tiles : num_sms;
     pl.smem = fixed + p.b_region + p.HS * halo_bytes;
-    // more than half of the shared memory keeps a second CTA (and its TMEM allocation) off the SM
+    // more than half of the shared memory keeps a second CTA like this one (and its TMEM allocation) off the SM
     if (pl.smem < 116 * 1024) pl.smem = 116 * 1024;
     pl.ok = pl.smem <= kSmemLimit;
     return pl;
@@ -705,8 +713,9 @@ StreamPlan plan_stream(int N, int H, int W, int Cin, int Cout, int K, int num_sm
     pl.bn = bn;
     pl.pair = pair;
     pl.smem = fixed + p.BS * b_bytes + p.HS * halo_bytes;
-    // more than half of the shared memory keeps a second CTA (and its TMEM allocation) off the SM
-    if (pl.smem < 116 * 1024) pl.smem = 116 * 1024;
+    // more than half of the shared memory keeps a second CTA like this one (and its TMEM allocation)
+    // off the SM; a pair, whose CTAs wait for one another, stays alone with its 512 columns
+    if (pl.smem < (pair ? kClusterAloneSmem : 116 * 1024)) pl.smem = pair ? kClusterAloneSmem : 116 * 1024;
     if (pair) {
         const int pairs = num_sms / 2;
         pl.grid = 2 * (p.num_tiles < pairs ? p.num_tiles : pairs);
@@ -770,6 +779,8 @@ int launch_dense_stream(const void *X, const void *F, void *Y, int Cin, int Cout
 using CfgBN64 = DenseTcCfg<64, 6>;
 using CfgBN128 = DenseTcCfg<128, 5>;
 using CfgBN256 = DenseTcCfg<256, 3>;
+static_assert(CfgBN128::SMEM_BYTES_PAIR >= kClusterAloneSmem && CfgBN256::SMEM_BYTES_PAIR >= kClusterAloneSmem,
+              "the pairs of 512 columns beside the short split form of the 8-bit product");
 
 // ---------------------------------------------------------------------------------------
 // Depthwise
@@ -1586,7 +1597,7 @@ HaloPadPlan plan_halo_pad(int N, int H, int W, int Cin, int Cout, const DenseGeo
     if (per > p.num_spatial) per = p.num_spatial;
     pl.grid = per * p.num_gn;
     pl.smem = fixed + static_cast<int>(b_res) + HS * p.halo_bytes;
-    // more than half of the shared memory keeps a second CTA (and its TMEM allocation) off the SM
+    // more than half of the shared memory keeps a second CTA like this one (and its TMEM allocation) off the SM
     if (pl.smem < 116 * 1024) pl.smem = 116 * 1024;
     pl.bn = bn;
     pl.ok = pl.smem <= kSmemLimit;

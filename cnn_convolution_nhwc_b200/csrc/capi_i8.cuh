@@ -343,10 +343,10 @@ int run_i8_product(const I8Operands &a, I8GemmParams p, cudaStream_t stream, Dev
                                   pl.split, d->num_sms);
     switch (pl.bn) {
         case 16:
-            return shared ? launch_i8_split<I8SplitCfg<16, 5, i8_slot_kblks(16, true)>, OUT>(a, p, pl.split, stream, d, bit + 3)
+            return shared ? launch_i8_split<I8ShortSplit16, OUT>(a, p, pl.split, stream, d, bit + 3)
                           : launch_i8_split<Split16, OUT>(a, p, pl.split, stream, d, bit + 2);
         case 32:
-            return shared ? launch_i8_split<I8SplitCfg<32, 4, i8_slot_kblks(32, true)>, OUT>(a, p, pl.split, stream, d, bit + 5)
+            return shared ? launch_i8_split<I8ShortSplit32, OUT>(a, p, pl.split, stream, d, bit + 5)
                           : launch_i8_split<Split32, OUT>(a, p, pl.split, stream, d, bit + 4);
         case 64: return launch_i8_split<Split64, OUT>(a, p, pl.split, stream, d, bit + 6);
         default: return launch_i8_split<Split128, OUT>(a, p, pl.split, stream, d, bit + 7);

@@ -83,6 +83,9 @@ struct I8SplitCfg {
     static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
 
+using I8ShortSplit16 = I8SplitCfg<16, 5, 1>;   // the short forms
+using I8ShortSplit32 = I8SplitCfg<32, 4, 1>;
+
 template <class Cfg, typename OUT>
 __global__ void __launch_bounds__(Cfg::THREADS)
 i8_split_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmQ, const I8GemmParams p,
