@@ -21,7 +21,6 @@ LIB = os.path.join(PKG, "libconv_b200.so")
 LIB_DEBUG = os.path.join(PKG, "libconv_b200_debug.so")
 MAIN = os.path.join(PKG, "csrc", "capi.cu")
 # the short host path of the 8-bit operators: a Python extension over torch's C++ tensors
-BINDING = os.path.join(PKG, "_binding_i8.so")
 BINDING_SRC = os.path.join(PKG, "csrc", "binding_i8.cpp")
 
 NVCC_FLAGS = [
@@ -73,18 +72,31 @@ def build(force: bool = False, verbose: bool = False, debug_bounds: bool = False
     return lib
 
 
+def binding_path() -> str:
+    """Where the Python extension for the running interpreter and torch lies. Both are in its name: it is
+    compiled against torch's C++ headers and Python's, so that one built for others must not be loaded."""
+    import sysconfig
+
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    key = f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}-abi{abi}"
+    return os.path.join(PKG, "_binding_i8." + "".join(c if c.isalnum() or c in "._+-" else "_" for c in key) + ".so")
+
+
 def build_binding(force: bool = False) -> str:
-    """Compile the Python extension of the 8-bit operators (csrc/binding_i8.cpp) against the torch
-    that runs, if it is missing or older than its source; returns its path."""
+    """Compile the Python extension of the 8-bit operators (csrc/binding_i8.cpp) against the torch and
+    the interpreter that run, if there is none for them or it is older than its source; returns its
+    path."""
+    lib = binding_path()
     with open(os.path.join(PKG, ".build.lock"), "w") as lk:
         fcntl.flock(lk, fcntl.LOCK_EX)
         try:
-            if force or not os.path.exists(BINDING) or os.path.getmtime(BINDING_SRC) > os.path.getmtime(BINDING):
+            if force or not os.path.exists(lib) or os.path.getmtime(BINDING_SRC) > os.path.getmtime(lib):
                 import sysconfig
 
                 import torch
                 base = os.path.dirname(torch.__file__)
-                tmp = BINDING + f".tmp{os.getpid()}"
+                tmp = lib + f".tmp{os.getpid()}"
                 cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
                        f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                        "-I" + os.path.join(base, "include"),
@@ -96,10 +108,10 @@ def build_binding(force: bool = False) -> str:
                 r = subprocess.run(cmd, capture_output=True, text=True)
                 if r.returncode != 0:
                     raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
-                os.replace(tmp, BINDING)
+                os.replace(tmp, lib)
         finally:
             fcntl.flock(lk, fcntl.LOCK_UN)
-    return BINDING
+    return lib
 
 
 if __name__ == "__main__":
