@@ -425,22 +425,42 @@ def dwpw_fwd(x, w_dw, b_dw, F, b_pw=None, y=None, stride=1, pad=0, dil=1, mode=D
 # A single-token call of these takes 2 to 5 us on the GPU, so the host's part counts. On the current
 # stream a call goes through _binding_i8 (csrc/binding_i8.cpp), which looks at the tensors in C++: 3
 # to 5 us with the outputs given. What it does not find in order, and a call with a stream named,
-# takes the checked way below, which says what is wrong.
+# takes the checked way below, which says what is wrong. The checked way needs no extension: where
+# none can be built or loaded (no compiler), every call takes it, after a warning.
 _BF16 = _F32 = _INT8 = _empty = _Tensor = _fast = None
 _ASK_SLOW = -1000
 
 
-def _i8_init():
-    global _BF16, _F32, _INT8, _empty, _Tensor, _fast
-    import importlib.util
+class _NoShortPath:
+    """In the extension's place where there is none: every call asks for the checked way."""
 
-    import torch
-    _BF16, _F32, _INT8, _empty, _Tensor = torch.bfloat16, torch.float32, torch.int8, torch.empty, torch.Tensor
+    @staticmethod
+    def _ask(*args):
+        return _ASK_SLOW
+
+    rmsnorm = rows = filter = dequant = pointwise = layer = _ask
+
+
+def _i8_extension():
+    import importlib.util
     spec = importlib.util.spec_from_file_location("_binding_i8", _build.build_binding())
     fast = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(fast)
     fast.bind(*(ctypes.cast(f, _P).value for f in (lib.rmsnorm_i8_fwd, lib.quant_rows_i8_fwd, lib.quant_filter_i8_fwd,
                                                    lib.dequant_rows_i8_fwd, lib.pointwise_i8_fwd, lib.conv2d_nhwc_fwd_i8)))
+    return fast
+
+
+def _i8_init():
+    global _BF16, _F32, _INT8, _empty, _Tensor, _fast
+    import torch
+    _BF16, _F32, _INT8, _empty, _Tensor = torch.bfloat16, torch.float32, torch.int8, torch.empty, torch.Tensor
+    try:
+        fast = _i8_extension()
+    except (RuntimeError, OSError, ImportError) as e:
+        import warnings
+        warnings.warn(f"the 8-bit operators run without their short host path: {e}", RuntimeWarning, stacklevel=3)
+        fast = _NoShortPath()
     _fast = fast
     return fast
 
