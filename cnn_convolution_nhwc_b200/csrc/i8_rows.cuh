@@ -276,13 +276,19 @@ __device__ __forceinline__ void i8_block_totals(uint32_t &amax, float &sum, uint
     }
 }
 
-// A row's scale as it is stored.
+// A row's scale as it is stored. A norm's A * rstd can pass the float32 range where the scale, which is
+// 127 times smaller, does not: then rstd is divided first.
 template <bool NORM>
 __device__ __forceinline__ float i8_stored_scale(uint32_t amax, float sum, bool finite, int C, float eps) {
     const float A = __uint_as_float(amax);
     if (!finite) return __uint_as_float(0x7fc00000u);
     if (amax == 0u) return 0.0f;
-    return NORM ? A * (1.0f / sqrtf(sum / static_cast<float>(C) + eps)) / 127.0f : A / 127.0f;
+    if constexpr (NORM) {
+        const float rstd = 1.0f / sqrtf(sum / static_cast<float>(C) + eps), top = A * rstd;
+        return top < __uint_as_float(0x7f800000u) ? top / 127.0f : A * (rstd / 127.0f);
+    } else {
+        return A / 127.0f;
+    }
 }
 
 // One row per group of threads: a block, or a warp (TPR = 32), which takes RW rows at once. A thread
