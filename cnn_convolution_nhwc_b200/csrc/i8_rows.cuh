@@ -294,7 +294,9 @@ __device__ __forceinline__ float i8_stored_scale(uint32_t amax, float sum, bool 
 // One row per group of threads: a block, or a warp (TPR = 32), which takes RW rows at once. A thread
 // holds NV groups of eight values of a row in registers, so a row of up to 8 * NV values a thread is
 // read once; a longer row (STREAM) is walked in pieces of that size twice, the second time from h
-// (or x), which the first pass left in L2. All of a thread's loads are issued before the first is
+// (or x), which the first pass left in L2. A streamed norm adds the pieces' sums of squares in
+// float64: a float32 sum that a thread carries through a row of 2^27 values (131072 additions) is off
+// by up to 1e-3 where the values are alike. All of a thread's loads are issued before the first is
 // used: with four groups a thread (of one row or several) that keeps 100 KB and more of loads in
 // flight per SM.
 // VEC: tensors on 16 bytes and C a multiple of 8; a thread's eight values are neighbours and move in
@@ -454,6 +456,7 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
 
     uint64_t t[RW][NV][4];
     uint64_t sum2[RW];      // of the squares, even and odd values apart
+    double pieces = 0.0;    // of a streamed row's earlier pieces
     float top[RW];          // the largest magnitude, or NaN
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
@@ -463,6 +466,12 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
     const int piece = tpr * 8 * NV;
     for (int c0 = 0; c0 < (STREAM ? C : 1); c0 += piece) {
         load(c0, true, t, sum2);
+        if constexpr (NORM && STREAM) {
+            float lo, hi;
+            f2_split(sum2[0], lo, hi);
+            pieces += static_cast<double>(lo) + static_cast<double>(hi);
+            sum2[0] = 0;
+        }
 #pragma unroll
         for (int r = 0; r < RW; ++r)
 #pragma unroll
@@ -484,7 +493,7 @@ i8_rows_kernel(const I8RowsParams p, unsigned int *status) {
         if constexpr (NORM) {
             float lo, hi;
             f2_split(sum2[r], lo, hi);
-            sum = lo + hi;
+            sum = STREAM ? static_cast<float>(pieces) : lo + hi;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         }

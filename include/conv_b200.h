@@ -296,7 +296,9 @@ int conv_i8_row_pitch(int C);
  *                    x or residual itself (updated in place); other overlaps are rejected
  *   weight         : float32 [C]
  *   q, scale       : 8-bit rows [M][ldq], float32 [M]
- * The sum of squares is float32; a row where it passes the float32 range has q = 0 and scale = NaN.
+ * The sum of squares is float32 (joined in float64 over the pieces of rows too long for a block's
+ * registers or shared memory), off by less than 2^-17 relative whatever C; a row where it passes the
+ * float32 range has q = 0 and scale = NaN.
  * Requirements: M, C >= 1; eps a normal positive float.
  */
 int rmsnorm_i8_fwd(const void *x, const void *residual, const float *weight, void *h, int8_t *q, float *scale,
