@@ -145,10 +145,13 @@ __device__ __forceinline__ void i8_pack(const uint64_t (&t)[4], I8Raw<float> &r)
 }
 
 // silu(a) * b for two pairs in float32, silu(a) = a / (1 + 2^(-a log2 e)), by the fast exponential and
-// reciprocal: relative error below 2^-22 + |a| 2^-24, far below the rounding to 8 bits (2^-8 of
-// the row's largest value) that follows. Gates below -87, whose silu is below 1.5e-36, give 0. With
-// an exponential and a quotient that keep denormals the gate took 14 instructions a value instead
-// of 4, and instructions bound the kernel.
+// reciprocal: relative error below (9 + 1.25 |a|) 2^-24, far below the rounding to 8 bits (2^-8 of
+// the row's largest value) that follows. In units of 2^-24 that is the rounded log2 e (0.224) and the
+// rounded product with it, which move the exponential by 1.224 |a|; the exponential 4 (two steps
+// of its last place), the addition 1, the reciprocal 2 (one step), and 1 for each product. Gates
+// below -87.33, whose exponential passes 2^126 and whose silu is below 1.04e-36, give 0. With an
+// exponential and a quotient that keep denormals the gate took 14 instructions a value instead of
+// 4, and instructions bound the kernel.
 __device__ __forceinline__ uint64_t i8_glu(uint64_t a, uint64_t b) {
     float lo, hi;
     f2_split(f2_mul(a, f2_pack(-1.44269504f, -1.44269504f)), lo, hi);

@@ -308,7 +308,7 @@ int rmsnorm_i8_fwd(const void *x, const void *residual, const float *weight, voi
  * 8-bit rows of activations: v = x (glu = 0, x is dtype [M][C]), or the gated product of a
  * feed-forward pair (glu = 1, x is dtype [M][2C], its halves gate and up):
  *     v[c] = silu(x[c]) * x[C + c],  silu(a) = a / (1 + exp(-a)), in float32 (relative error below
- * 2^-22 + |a| 2^-24; gates below -87, whose silu is below 1.5e-36 in magnitude, give 0).
+ * (9 + 1.25 |x[c]|) 2^-24; gates below -87.33, whose silu is below 1.04e-36 in magnitude, give 0).
  * Also quantises a filter stored [Cout][Cin] (a row per output channel).
  */
 int quant_rows_i8_fwd(const void *x, int8_t *q, float *scale, int M, int C, int ldq, int glu, int dtype,
