@@ -63,11 +63,15 @@ int run_i8_rows(const I8RowsParams &p, cudaStream_t stream, DeviceState *d) {
         if constexpr (MODE == kI8Glu) {
             if (C <= 8192)
                 return launch_i8_rows<T, MODE, 2, true, 0, 1, false>(p, (C + 511) / 512 * 32, stream, d);
-            // three groups (56 registers a thread) unless four (64) let more rows be on an SM: 8192 x 9216
-            // in bf16 60.6 us with three and 67.2 with four, 8192 x 10240 80.1 and 71.7
-            const int threads = (C + 767) / 768 * 32, threads4 = (C + 1023) / 1024 * 32;
-            if (C <= 12288 && 65536 / (threads * 56) >= 65536 / (threads4 * 64))
-                return launch_i8_rows<T, MODE, 3, true, 0, 1, false>(p, threads, stream, d);
+            // bf16: three groups (52 registers a thread, allocated as 56) unless four (64) let more rows be on
+            // an SM: 8192 x 9216 59.6 us with three and 66.0 with four, 8192 x 10240 78.0 and 70.3, 8192 x
+            // 12288 84.5 and 92.7. In float32 three take as many registers as four: 8192 x 9216 113.5 and
+            // 97.4, 8192 x 12288 131 and 131
+            if constexpr (sizeof(T) == 2) {
+                const int threads = (C + 767) / 768 * 32, threads4 = (C + 1023) / 1024 * 32;
+                if (C <= 12288 && 65536 / (threads * 56) >= 65536 / (threads4 * 64))
+                    return launch_i8_rows<T, MODE, 3, true, 0, 1, false>(p, threads, stream, d);
+            }
         }
         if (C <= 16384) return launch_i8_rows<T, MODE, 4, true, 0, 1, false>(p, (C + 1023) / 1024 * 32, stream, d);
         return launch_i8_rows<T, MODE, 4, true, 0, 1, true>(p, 512, stream, d);
