@@ -284,7 +284,7 @@ struct I8DequantParams {
 __device__ __forceinline__ void i8_put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void i8_put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// y = q * scale, one rounding. A warp takes a segment of a row, four accesses a lane in flight: 16
+// y = q * scale in float32, rounded to the type. A warp takes a segment of a row, four accesses a lane in flight: 16
 // bytes of y each (VEC: rows of y on 16 bytes), so that the warp's stores are whole lines; else 16
 // values a lane, one of every 32. blockIdx.y counts the segments that do not fit in one block.
 template <typename T, bool VEC>

@@ -257,7 +257,8 @@ int dwpw_fwd(const float *x, const float *w_dw, const float *b_dw, const void *F
  * both operands held as signed bytes: a scale per row (token) of the activations and per output
  * channel of the filter. These have no counterpart on the pages; they extend conv2d_nhwc_fwd at
  * K = 1, where a byte instead of a bf16 value halves the filter's traffic and doubles the tensor
- * cores' rate.
+ * cores' rate. That pays from 512 input channels on, and for few pixels; with 256 channels and fewer
+ * and many pixels conv2d_nhwc_fwd is faster.
  *
  * 8-bit rows: a matrix of M rows of C bytes is int8_t q[M][ld] with ld >= C bytes from row to
  * row, ld a multiple of 16 and q 16-byte aligned. conv_i8_row_pitch(C) is the ld to take, C rounded
@@ -322,7 +323,7 @@ int quant_rows_i8_fwd(const void *x, int8_t *q, float *scale, int M, int C, int 
 int quant_filter_i8_fwd(const void *F, int8_t *Wq, float *scale, int Cin, int Cout, int ldw, int dtype,
                         cudaStream_t stream);
 
-/* Reads 8-bit rows back: y[m][c] = q[m][c] * scale[m] rounded to dtype; y is [M][C], contiguous. */
+/* Reads 8-bit rows back: y[m][c] = q[m][c] * scale[m] in float32, rounded to dtype; y is [M][C], contiguous. */
 int dequant_rows_i8_fwd(const int8_t *q, const float *scale, void *y, int M, int C, int ldq, int dtype,
                         cudaStream_t stream);
 
