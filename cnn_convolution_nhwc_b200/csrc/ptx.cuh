@@ -64,11 +64,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 // dependents launch as soon as it starts (grid_dependents_launch) and, before its first
 // global-memory access, waits until every kernel it depends on has completed and its memory
 // operations are visible (grid_dependency_wait) -- so a chain of dependent convolutions keeps
-// stream order, and only launch latency and what comes before the wait in a kernel (barrier
-// set-up, tensor-map prefetch) overlap the previous kernel's tail. TMEM is allocated after the
-// wait: a CTA that held columns while it waited could leave too few for a predecessor's CTA on its
-// SM, which lets its dependents launch before it allocates, and neither would ever end. Both are
-// no-ops for a kernel launched without the attribute.
+// stream order, and only launch latency and the on-chip prologue (barrier set-up, TMEM
+// allocation, tensor-map prefetch) overlap the previous kernel's tail. Both are no-ops for a
+// kernel launched without the attribute.
 __device__ __forceinline__ void grid_dependents_launch() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
