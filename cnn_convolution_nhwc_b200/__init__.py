@@ -326,6 +326,8 @@ def conv2d_nhwc_fwd_im2col(X, F, Y=None, workspace=None, stream=None):
         raise ValueError("workspace must be a contiguous CUDA tensor")
     if Y is None:
         Y = _empty_on(stream, (N, H - K + 1, W - K + 1, Cout), torch.bfloat16, X.device)
+    elif tuple(Y.shape) != (N, H - K + 1, W - K + 1, Cout):
+        raise ValueError("Y has the wrong shape")
     py = _tensor(Y, torch.bfloat16, 4, "Y")
     _call(lib.conv2d_nhwc_fwd_im2col, "conv2d_nhwc_fwd_im2col", (X, F, Y, workspace), stream,
           px, pf, py, ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size(),
